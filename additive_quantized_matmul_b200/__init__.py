@@ -25,6 +25,10 @@ __all__ = [
     "aq_param_grad", "aq_encode_workspace_bytes", "aq_encode", "aq_gather_probe_sink_bytes",
     "aq_gather_probe", "EXPORTED_SYMBOLS",
     "GEMV_NOALLOC_SCRATCH_BYTES",
+    "ACTIVATIONS", "Epilogue", "Weights", "aq_gemm_fused_workspace_bytes", "aq_gemv_fused", "aq_gemm_fused",
+    "aq_input_grad_workspace_bytes", "aq_input_grad", "aq_gemm_fused_grad_workspace_bytes", "aq_gemm_fused_grad",
+    "aq_glu_gemv_workspace_bytes", "aq_glu_gemm_workspace_bytes", "aq_glu_gemv", "aq_glu_gemm",
+    "aq_glu_grad_workspace_bytes", "aq_glu_grad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,7 +47,13 @@ EXPORTED_SYMBOLS = (
     "aq_gemm_ordered",
     "aq_param_grad_workspace_bytes", "aq_param_grad", "aq_encode_workspace_bytes", "aq_encode",
     "aq_gather_probe_sink_bytes", "aq_gather_probe",
+    "aq_gemm_fused_workspace_bytes", "aq_gemv_fused", "aq_gemm_fused", "aq_input_grad_workspace_bytes",
+    "aq_input_grad", "aq_gemm_fused_grad_workspace_bytes", "aq_gemm_fused_grad", "aq_glu_gemv_workspace_bytes",
+    "aq_glu_gemm_workspace_bytes", "aq_glu_gemv", "aq_glu_gemm", "aq_glu_grad_workspace_bytes", "aq_glu_grad",
 )
+
+# aq_activation of include/aq.h, by name.
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # AQ_GEMV_NOALLOC_SCRATCH_BYTES of include/aq.h: the fixed scratch behind
 # aq_gemv_noalloc.
@@ -70,6 +80,25 @@ class LayerDesc(ctypes.Structure):
         return cls(out_features, in_features, group_size, num_codebooks, nbits)
 
 
+class Epilogue(ctypes.Structure):
+    """``aq_epilogue``: activation, bias [out] or None, residual [out][n] or None."""
+
+    _fields_ = [("activation", ctypes.c_int32), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p)]
+
+
+class Weights(ctypes.Structure):
+    """``aq_weights``: packed codes, codebooks and scales of one layer."""
+
+    _fields_ = [("packed", ctypes.c_void_p), ("codebooks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+    @classmethod
+    def make(cls, packed, codebooks, scales=None) -> "Weights":
+        """Addresses of the three arrays, which the structure keeps alive."""
+        w = cls(_ptr(packed), _ptr(codebooks), _ptr(scales))
+        w.arrays = (packed, codebooks, scales)
+        return w
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(library_path):
         raise ImportError(
@@ -77,7 +106,7 @@ def _load() -> ctypes.CDLL:
             "`python additive_quantized_matmul_b200/build.py` (nvcc, sm_100a)")
     L = ctypes.CDLL(library_path)
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
-    dp = ctypes.POINTER(LayerDesc)
+    dp, ep, wp = ctypes.POINTER(LayerDesc), ctypes.POINTER(Epilogue), ctypes.POINTER(Weights)
     sig = {
         "aq_status_string": ([i32], ctypes.c_char_p),
         "aq_version": ([], i32),
@@ -100,6 +129,19 @@ def _load() -> ctypes.CDLL:
         "aq_encode": ([dp, vp, vp, vp, vp, i32, vp, vp, sz, vp], i32),
         "aq_gather_probe_sink_bytes": ([i32], sz),
         "aq_gather_probe": ([vp, vp, sz, i32, vp, vp], i32),
+        "aq_gemm_fused_workspace_bytes": ([dp, i32], sz),
+        "aq_gemv_fused": ([dp, vp, vp, vp, vp, i32, ep, vp, vp, sz, vp], i32),
+        "aq_gemm_fused": ([dp, vp, vp, vp, vp, i32, ep, vp, vp, sz, vp], i32),
+        "aq_input_grad_workspace_bytes": ([dp, i32], sz),
+        "aq_input_grad": ([dp, vp, vp, vp, vp, i32, vp, vp, sz, vp], i32),
+        "aq_gemm_fused_grad_workspace_bytes": ([dp, i32], sz),
+        "aq_gemm_fused_grad": ([dp, vp, vp, vp, vp, vp, i32, ep, vp, vp, vp, vp, sz, vp], i32),
+        "aq_glu_gemv_workspace_bytes": ([dp, i32], sz),
+        "aq_glu_gemm_workspace_bytes": ([dp, i32], sz),
+        "aq_glu_gemv": ([dp, wp, wp, vp, i32, i32, vp, vp, sz, vp], i32),
+        "aq_glu_gemm": ([dp, wp, wp, vp, i32, i32, vp, vp, sz, vp], i32),
+        "aq_glu_grad_workspace_bytes": ([dp, i32], sz),
+        "aq_glu_grad": ([dp, wp, wp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp], i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -271,3 +313,104 @@ def aq_gather_probe(codebook, codes, n: int, mode: int, sink, stream=None) -> No
     each code handled by the CTA holding its slice); per-thread XOR
     checksums go to ``sink``."""
     _check("aq_gather_probe", lib.aq_gather_probe(_ptr(codebook), _ptr(codes), n, mode, _ptr(sink), _stream(stream)))
+
+
+def aq_gemm_fused_workspace_bytes(desc: LayerDesc, T: int) -> int:
+    return lib.aq_gemm_fused_workspace_bytes(ctypes.byref(desc), T)
+
+
+def aq_gemv_fused(desc: LayerDesc, packed, codebooks, scales, x, batch: int, y, workspace,
+                  workspace_bytes: int | None = None, stream=None, *, activation: int = 0, bias=None,
+                  residual=None) -> None:
+    """y = act(diag(s) W x + bias) + residual for batch 1..16 (activation: a
+    value of ACTIVATIONS; ``y`` may be ``residual``); the workspace is
+    aq_gemv's."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_gemv_fused", lib.aq_gemv_fused(ctypes.byref(desc), _ptr(packed), _ptr(codebooks), _ptr(scales),
+                                              _ptr(x), batch, Epilogue(activation, _ptr(bias), _ptr(residual)),
+                                              _ptr(y), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def aq_gemm_fused(desc: LayerDesc, packed, codebooks, scales, x, T: int, y, workspace,
+                  workspace_bytes: int | None = None, stream=None, *, activation: int = 0, bias=None,
+                  residual=None) -> None:
+    """aq_gemv_fused for any token count."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_gemm_fused", lib.aq_gemm_fused(ctypes.byref(desc), _ptr(packed), _ptr(codebooks), _ptr(scales),
+                                              _ptr(x), T, Epilogue(activation, _ptr(bias), _ptr(residual)),
+                                              _ptr(y), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def aq_input_grad_workspace_bytes(desc: LayerDesc, T: int) -> int:
+    return lib.aq_input_grad_workspace_bytes(ctypes.byref(desc), T)
+
+
+def aq_input_grad(desc: LayerDesc, packed, codebooks, scales, gy, T: int, gx, workspace,
+                  workspace_bytes: int | None = None, stream=None) -> None:
+    """gx = W^T (s * gy): dL/dx [in][T] from dL/dy [out][T]."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_input_grad", lib.aq_input_grad(ctypes.byref(desc), _ptr(packed), _ptr(codebooks), _ptr(scales),
+                                              _ptr(gy), T, _ptr(gx), _ptr(workspace), workspace_bytes,
+                                              _stream(stream)))
+
+
+def aq_gemm_fused_grad_workspace_bytes(desc: LayerDesc, T: int) -> int:
+    return lib.aq_gemm_fused_grad_workspace_bytes(ctypes.byref(desc), T)
+
+
+def aq_gemm_fused_grad(desc: LayerDesc, packed, codebooks, scales, x, gy, T: int, grad_z, grad_bias, grad_x,
+                       workspace, workspace_bytes: int | None = None, stream=None, *, activation: int = 0,
+                       bias=None) -> None:
+    """Backward of aq_gemm_fused: grad_z [out][T] (before the activation),
+    grad_bias [out] fp32 and grad_x [in][T] (either may be None)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_gemm_fused_grad",
+           lib.aq_gemm_fused_grad(ctypes.byref(desc), _ptr(packed), _ptr(codebooks), _ptr(scales), _ptr(x),
+                                  _ptr(gy), T, Epilogue(activation, _ptr(bias), None), _ptr(grad_z),
+                                  _ptr(grad_bias), _ptr(grad_x), _ptr(workspace), workspace_bytes,
+                                  _stream(stream)))
+
+
+def aq_glu_gemv_workspace_bytes(desc: LayerDesc, batch: int) -> int:
+    return lib.aq_glu_gemv_workspace_bytes(ctypes.byref(desc), batch)
+
+
+def aq_glu_gemm_workspace_bytes(desc: LayerDesc, T: int) -> int:
+    return lib.aq_glu_gemm_workspace_bytes(ctypes.byref(desc), T)
+
+
+def aq_glu_gemv(desc: LayerDesc, gate: Weights, up: Weights, x, batch: int, activation: int, y, workspace,
+                workspace_bytes: int | None = None, stream=None) -> None:
+    """y = act(gate(x)) * up(x) for batch 1..16, both layers of ``desc``."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_glu_gemv", lib.aq_glu_gemv(ctypes.byref(desc), gate, up, _ptr(x), batch, activation, _ptr(y),
+                                          _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def aq_glu_gemm(desc: LayerDesc, gate: Weights, up: Weights, x, T: int, activation: int, y, workspace,
+                workspace_bytes: int | None = None, stream=None) -> None:
+    """aq_glu_gemv for any token count."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_glu_gemm", lib.aq_glu_gemm(ctypes.byref(desc), gate, up, _ptr(x), T, activation, _ptr(y),
+                                          _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def aq_glu_grad_workspace_bytes(desc: LayerDesc, T: int) -> int:
+    return lib.aq_glu_grad_workspace_bytes(ctypes.byref(desc), T)
+
+
+def aq_glu_grad(desc: LayerDesc, gate: Weights, up: Weights, x, gy, T: int, activation: int, grad_gate, grad_up,
+                grad_x, workspace, workspace_bytes: int | None = None, stream=None) -> None:
+    """Backward of the gated block: grad_gate and grad_up [out][T] (of the two
+    projections' outputs) and grad_x [in][T] (None to skip)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("aq_glu_grad", lib.aq_glu_grad(ctypes.byref(desc), gate, up, _ptr(x), _ptr(gy), T, activation,
+                                          _ptr(grad_gate), _ptr(grad_up), _ptr(grad_x), _ptr(workspace),
+                                          workspace_bytes, _stream(stream)))

@@ -4,6 +4,7 @@
 // GPU; on error nothing is launched.  No exception crosses the interface.
 #include <stdint.h>
 
+#include "epilogue.cuh"
 #include "scheme.cuh"
 
 namespace {
@@ -284,6 +285,220 @@ aq_status aq_gather_probe(const uint16_t *codebook, const uint16_t *codes, size_
     if ((codebook && !aligned16(codebook)) || !aligned16(codes) || !aligned16(sink)) return AQ_ERR_MISALIGNED;
     return from_cuda(
         aqh::launch_gather_probe(codebook, codes, n, mode, sink, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- layer operators ---------------------------------------------------------
+
+namespace {
+
+bool act_ok(int act) { return act >= AQ_ACT_NONE && act <= AQ_ACT_SILU; }
+
+constexpr int kMaxTokens = 1 << 22;
+constexpr int32_t kGluGemvMaxOut = 131072;  // 1024 arrival counters of 128 rows
+
+aq_status check_weights(const void *packed, const uint16_t *codebooks, const uint16_t *scales)
+{
+    if (!packed || !codebooks) return AQ_ERR_INVALID_ARG;
+    if (!aligned16(packed) || !aligned16(codebooks)) return AQ_ERR_MISALIGNED;
+    if (scales && (reinterpret_cast<uintptr_t>(scales) & 1u)) return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+aqk::LayerWeights layer_weights(const void *packed, const uint16_t *codebooks, const uint16_t *scales)
+{
+    return {reinterpret_cast<const uint8_t *>(packed), reinterpret_cast<const uint4 *>(codebooks), scales};
+}
+
+// Bias and residual of an epilogue (the residual only where it is used).
+aq_status check_epilogue(const aq_epilogue *ep, bool with_residual, aqk::EpilogueArgs *out)
+{
+    *out = {AQ_ACT_NONE, nullptr, nullptr};
+    if (!ep) return AQ_OK;
+    if (!act_ok(ep->activation)) return AQ_ERR_INVALID_ARG;
+    if (ep->bias && (reinterpret_cast<uintptr_t>(ep->bias) & 1u)) return AQ_ERR_MISALIGNED;
+    if (with_residual && ep->residual && !aligned16(ep->residual)) return AQ_ERR_MISALIGNED;
+    *out = {ep->activation, ep->bias, with_residual ? ep->residual : nullptr};
+    return AQ_OK;
+}
+
+aq_status check_workspace(const void *workspace, size_t workspace_bytes, size_t need)
+{
+    if (!workspace || workspace_bytes < need) return AQ_ERR_WORKSPACE;
+    return aligned16(workspace) ? AQ_OK : AQ_ERR_MISALIGNED;
+}
+
+// aq_gemv_fused (n <= 16) and aq_gemm_fused
+aq_status fused_entry(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                      const uint16_t *scales, const uint16_t *x, int n, int max_n, const aq_epilogue *ep, uint16_t *y,
+                      void *workspace, size_t workspace_bytes, aq_stream_t stream)
+{
+    aq_status st = check_desc(desc);
+    if (st != AQ_OK) return st;
+    if (n < 1 || n > max_n || !x || !y || x == y) return AQ_ERR_INVALID_ARG;
+    if ((st = check_weights(packed, codebooks, scales)) != AQ_OK) return st;
+    if (!aligned16(x) || !aligned16(y)) return AQ_ERR_MISALIGNED;
+    aqk::EpilogueArgs e;
+    if ((st = check_epilogue(ep, true, &e)) != AQ_OK) return st;
+    const Geom g = aqk::make_geom(*desc);
+    const bool gemv = max_n == 16;
+    const size_t need = gemv ? aqh::gemv_workspace_bytes(g, n) : aqh::gemm_fused_workspace_bytes(g, n);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != AQ_OK) return st;
+    const aqk::LayerWeights w = layer_weights(packed, codebooks, scales);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(gemv ? aqh::launch_gemv_fused(g, w, x, n, e, y, workspace, s)
+                          : aqh::launch_gemm_fused(g, w, x, n, e, y, workspace, s));
+}
+
+// aq_glu_gemv (n <= 16) and aq_glu_gemm
+aq_status glu_entry(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x, int n,
+                    int max_n, int activation, uint16_t *y, void *workspace, size_t workspace_bytes,
+                    aq_stream_t stream)
+{
+    aq_status st = check_desc(desc);
+    if (st != AQ_OK) return st;
+    const bool gemv = max_n == 16;
+    if (gemv && desc->out_features > kGluGemvMaxOut) return AQ_ERR_INVALID_ARG;
+    if (n < 1 || n > max_n || !gate || !up || !x || !y || x == y || !act_ok(activation)) return AQ_ERR_INVALID_ARG;
+    if ((st = check_weights(gate->packed, gate->codebooks, gate->scales)) != AQ_OK) return st;
+    if ((st = check_weights(up->packed, up->codebooks, up->scales)) != AQ_OK) return st;
+    if (!aligned16(x) || !aligned16(y)) return AQ_ERR_MISALIGNED;
+    const Geom g = aqk::make_geom(*desc);
+    const size_t need = gemv ? aqh::glu_gemv_workspace_bytes(g, n) : aqh::glu_gemm_workspace_bytes(g, n);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != AQ_OK) return st;
+    const aqk::LayerWeights wg = layer_weights(gate->packed, gate->codebooks, gate->scales);
+    const aqk::LayerWeights wu = layer_weights(up->packed, up->codebooks, up->scales);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(gemv ? aqh::launch_glu_gemv(g, wg, wu, x, n, activation, y, workspace, s)
+                          : aqh::launch_glu_gemm(g, wg, wu, x, n, activation, y, workspace, s));
+}
+
+}  // namespace
+
+size_t aq_gemm_fused_workspace_bytes(const aq_layer_desc *desc, int T)
+{
+    if (check_desc(desc) != AQ_OK || T < 1 || T > kMaxTokens) return 0;
+    return aqh::gemm_fused_workspace_bytes(aqk::make_geom(*desc), T);
+}
+
+aq_status aq_gemv_fused(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *x, int batch, const aq_epilogue *ep, uint16_t *y,
+                        void *workspace, size_t workspace_bytes, aq_stream_t stream)
+{
+    return fused_entry(desc, packed, codebooks, scales, x, batch, 16, ep, y, workspace, workspace_bytes, stream);
+}
+
+aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *x, int T, const aq_epilogue *ep, uint16_t *y,
+                        void *workspace, size_t workspace_bytes, aq_stream_t stream)
+{
+    return fused_entry(desc, packed, codebooks, scales, x, T, kMaxTokens, ep, y, workspace, workspace_bytes, stream);
+}
+
+size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T)
+{
+    if (check_desc(desc) != AQ_OK || T < 1 || T > kMaxTokens) return 0;
+    return aqh::input_grad_workspace_bytes(aqk::make_geom(*desc), T);
+}
+
+aq_status aq_input_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *gy, int T, uint16_t *gx, void *workspace,
+                        size_t workspace_bytes, aq_stream_t stream)
+{
+    aq_status st = check_desc(desc);
+    if (st != AQ_OK) return st;
+    if (T < 1 || T > kMaxTokens || !gy || !gx || gy == gx) return AQ_ERR_INVALID_ARG;
+    if ((st = check_weights(packed, codebooks, scales)) != AQ_OK) return st;
+    if (!aligned16(gy) || !aligned16(gx)) return AQ_ERR_MISALIGNED;
+    const Geom g = aqk::make_geom(*desc);
+    if ((st = check_workspace(workspace, workspace_bytes, aqh::input_grad_workspace_bytes(g, T))) != AQ_OK) return st;
+    return from_cuda(aqh::launch_input_grad(g, layer_weights(packed, codebooks, scales), gy, T, gx, workspace,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t aq_gemm_fused_grad_workspace_bytes(const aq_layer_desc *desc, int T)
+{
+    if (check_desc(desc) != AQ_OK || T < 1 || T > kMaxTokens) return 0;
+    return aqh::gemm_fused_grad_workspace_bytes(aqk::make_geom(*desc), T);
+}
+
+aq_status aq_gemm_fused_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                             const uint16_t *scales, const uint16_t *x, const uint16_t *gy, int T,
+                             const aq_epilogue *ep, uint16_t *grad_z, float *grad_bias, uint16_t *grad_x,
+                             void *workspace, size_t workspace_bytes, aq_stream_t stream)
+{
+    aq_status st = check_desc(desc);
+    if (st != AQ_OK) return st;
+    if (T < 1 || T > kMaxTokens || !x || !gy || !grad_z) return AQ_ERR_INVALID_ARG;
+    if (grad_z == x || grad_z == gy || (grad_x && (grad_x == x || grad_x == gy || grad_x == grad_z)))
+        return AQ_ERR_INVALID_ARG;
+    if ((st = check_weights(packed, codebooks, scales)) != AQ_OK) return st;
+    if (!aligned16(x) || !aligned16(gy) || !aligned16(grad_z) || (grad_bias && !aligned16(grad_bias)) ||
+        (grad_x && !aligned16(grad_x)))
+        return AQ_ERR_MISALIGNED;
+    aqk::EpilogueArgs e;
+    if ((st = check_epilogue(ep, false, &e)) != AQ_OK) return st;
+    const Geom g = aqk::make_geom(*desc);
+    if ((st = check_workspace(workspace, workspace_bytes, aqh::gemm_fused_grad_workspace_bytes(g, T))) != AQ_OK)
+        return st;
+    return from_cuda(aqh::launch_gemm_fused_grad(g, layer_weights(packed, codebooks, scales), x, gy, T, e, grad_z,
+                                                 grad_bias, grad_x, workspace,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t aq_glu_gemv_workspace_bytes(const aq_layer_desc *desc, int batch)
+{
+    if (check_desc(desc) != AQ_OK || batch < 1 || batch > 16 || desc->out_features > kGluGemvMaxOut) return 0;
+    return aqh::glu_gemv_workspace_bytes(aqk::make_geom(*desc), batch);
+}
+
+size_t aq_glu_gemm_workspace_bytes(const aq_layer_desc *desc, int T)
+{
+    if (check_desc(desc) != AQ_OK || T < 1 || T > kMaxTokens) return 0;
+    return aqh::glu_gemm_workspace_bytes(aqk::make_geom(*desc), T);
+}
+
+aq_status aq_glu_gemv(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      int batch, int activation, uint16_t *y, void *workspace, size_t workspace_bytes,
+                      aq_stream_t stream)
+{
+    return glu_entry(desc, gate, up, x, batch, 16, activation, y, workspace, workspace_bytes, stream);
+}
+
+aq_status aq_glu_gemm(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      int T, int activation, uint16_t *y, void *workspace, size_t workspace_bytes,
+                      aq_stream_t stream)
+{
+    return glu_entry(desc, gate, up, x, T, kMaxTokens, activation, y, workspace, workspace_bytes, stream);
+}
+
+size_t aq_glu_grad_workspace_bytes(const aq_layer_desc *desc, int T)
+{
+    if (check_desc(desc) != AQ_OK || T < 1 || T > kMaxTokens) return 0;
+    return aqh::glu_grad_workspace_bytes(aqk::make_geom(*desc), T);
+}
+
+aq_status aq_glu_grad(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      const uint16_t *gy, int T, int activation, uint16_t *grad_gate, uint16_t *grad_up,
+                      uint16_t *grad_x, void *workspace, size_t workspace_bytes, aq_stream_t stream)
+{
+    aq_status st = check_desc(desc);
+    if (st != AQ_OK) return st;
+    if (T < 1 || T > kMaxTokens || !gate || !up || !x || !gy || !grad_gate || !grad_up || !act_ok(activation))
+        return AQ_ERR_INVALID_ARG;
+    if (grad_gate == grad_up || grad_gate == x || grad_gate == gy || grad_up == x || grad_up == gy ||
+        (grad_x && (grad_x == x || grad_x == gy || grad_x == grad_gate || grad_x == grad_up)))
+        return AQ_ERR_INVALID_ARG;
+    if ((st = check_weights(gate->packed, gate->codebooks, gate->scales)) != AQ_OK) return st;
+    if ((st = check_weights(up->packed, up->codebooks, up->scales)) != AQ_OK) return st;
+    if (!aligned16(x) || !aligned16(gy) || !aligned16(grad_gate) || !aligned16(grad_up) ||
+        (grad_x && !aligned16(grad_x)))
+        return AQ_ERR_MISALIGNED;
+    const Geom g = aqk::make_geom(*desc);
+    if ((st = check_workspace(workspace, workspace_bytes, aqh::glu_grad_workspace_bytes(g, T))) != AQ_OK) return st;
+    return from_cuda(aqh::launch_glu_grad(g, layer_weights(gate->packed, gate->codebooks, gate->scales),
+                                          layer_weights(up->packed, up->codebooks, up->scales), x, gy, T, activation,
+                                          grad_gate, grad_up, grad_x, workspace,
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

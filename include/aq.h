@@ -341,6 +341,129 @@ aq_status aq_param_grad(const aq_layer_desc *desc, const void *packed, const uin
                         size_t workspace_bytes, aq_stream_t stream);
 
 /*
+ * Layer operators: the products a transformer block makes of quantised
+ * layers, with what stands around them.  All activations are binary16,
+ * [features][tokens] row-major, like x and y above; sums are fp32, and each
+ * result is rounded once where it is written.
+ */
+
+/* Activation functions; z in fp32, NaN stays NaN. */
+typedef enum {
+    AQ_ACT_NONE = 0,      /* z                                                   */
+    AQ_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0                             */
+    AQ_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function      */
+    AQ_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2     */
+    AQ_ACT_SILU = 4       /* z / (1 + exp(-z))                                   */
+} aq_activation;
+
+/* What follows a product: y = RN16(act(s (W x) + bias) + residual). */
+typedef struct {
+    int32_t activation;       /* aq_activation                                     */
+    const uint16_t *bias;     /* [out] binary16 or NULL (2-byte alignment)         */
+    const uint16_t *residual; /* [out][n] binary16 or NULL; may be y itself        */
+} aq_epilogue;
+
+/* The stored weights of one layer, as the products above take them. */
+typedef struct {
+    const void *packed;        /* from aq_pack_codes                                */
+    const uint16_t *codebooks; /* [K][2^B][8] binary16                              */
+    const uint16_t *scales;    /* [out] binary16, or NULL for s = 1                 */
+} aq_weights;
+
+/*
+ * aq_gemv and aq_gemm with an epilogue:
+ *   z[o][b] = s[o] * sum_i W[o][i] x[i][b] + bias[o]
+ *   y[o][b] = RN16(act(z[o][b]) + residual[o][b]).
+ * aq_gemv_fused takes batch 1..16 and a workspace of aq_gemv_workspace_bytes,
+ * aq_gemm_fused 1 <= T <= 2^22 tokens and one of
+ * aq_gemm_fused_workspace_bytes.  `ep` NULL means no bias, no activation, no
+ * residual.  y may be the residual array itself (each element is read before
+ * it is written, by the thread that writes it) but overlaps no other input.
+ * Other arguments, determinism, programmatic launch and early weight reads
+ * as for aq_gemv and aq_gemm; bias and residual are read only after the
+ * previous work on the stream.  AQ_ERR_INVALID_ARG for an unknown
+ * activation or y = x; AQ_ERR_MISALIGNED for a residual off a 16-byte or a
+ * bias off a 2-byte boundary.
+ */
+size_t aq_gemm_fused_workspace_bytes(const aq_layer_desc *desc, int T);
+aq_status aq_gemv_fused(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *x, int batch, const aq_epilogue *ep, uint16_t *y,
+                        void *workspace, size_t workspace_bytes, aq_stream_t stream);
+aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *x, int T, const aq_epilogue *ep, uint16_t *y,
+                        void *workspace, size_t workspace_bytes, aq_stream_t stream);
+
+/*
+ * Input gradient of a layer, the transposed product: for L = sum(gy * y) with
+ * y = diag(s) W x,
+ *   gx[i][t] = RN16(sum_o W[o][i] s[o] gy[o][t]),   gy [out][T], gx [in][T],
+ * 1 <= T <= 2^22.  The tensor cores multiply gy by RN16(s[o] 2^-E W[o][i]),
+ * where 2^E is the power of two just above the largest |s| (so that no
+ * weight overflows and small scales lose no bits), and 2^E is applied to the
+ * fp32 sum: each weight carries one rounding of at most 2^-11 of its value
+ * plus 2^(E-25).  gx overlaps no input.  Together with aq_param_grad this is
+ * the backward pass of aq_gemm.  Deterministic; the workspace holds
+ * aq_input_grad_workspace_bytes(desc, T) bytes.
+ */
+size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T);
+aq_status aq_input_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                        const uint16_t *scales, const uint16_t *gy, int T, uint16_t *gx, void *workspace,
+                        size_t workspace_bytes, aq_stream_t stream);
+
+/*
+ * Backward pass of aq_gemm_fused (and of aq_gemv_fused) from its input; the
+ * pre-activation z is computed again.  With gy = dL/dy [out][T]:
+ *   grad_z[o][t]  = RN16(gy[o][t] act'(z[o][t]))        [out][T] binary16
+ *   grad_bias[o]  = sum_t gy[o][t] act'(z[o][t])        [out] fp32, NULL to skip
+ *   grad_x[i][t]  = RN16(sum_o W[o][i] s[o] grad_z[o][t]) [in][T], NULL to skip
+ * (the rounded grad_z, as aq_input_grad would be given).  The residual's
+ * gradient is gy itself; aq_param_grad(x, grad_z) gives the scales' and
+ * codebooks'.  ep->residual is ignored.  The sums of grad_bias take a fixed
+ * order: deterministic.  1 <= T <= 2^22.  The outputs overlap no input and
+ * not one another.
+ */
+size_t aq_gemm_fused_grad_workspace_bytes(const aq_layer_desc *desc, int T);
+aq_status aq_gemm_fused_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
+                             const uint16_t *scales, const uint16_t *x, const uint16_t *gy, int T,
+                             const aq_epilogue *ep, uint16_t *grad_z, float *grad_bias, uint16_t *grad_x,
+                             void *workspace, size_t workspace_bytes, aq_stream_t stream);
+
+/*
+ * Gated feed-forward block, both projections in one kernel:
+ *   g = s_g (W_g x),  u = s_u (W_u x),  y[o][b] = RN16(act(g[o][b]) u[o][b]),
+ * for two layers of the same descriptor.  aq_glu_gemv takes batch 1..16 and
+ * out <= 131072 (its two projections meet at one arrival counter per 128
+ * rows; AQ_ERR_INVALID_ARG above), aq_glu_gemm 1 <= T <= 2^22 tokens.
+ * `activation` is an aq_activation, applied to the gate.  y overlaps no input.  Launch,
+ * early weight reads (of both layers) and determinism as for aq_gemv and
+ * aq_gemm.
+ */
+size_t aq_glu_gemv_workspace_bytes(const aq_layer_desc *desc, int batch);
+size_t aq_glu_gemm_workspace_bytes(const aq_layer_desc *desc, int T);
+aq_status aq_glu_gemv(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      int batch, int activation, uint16_t *y, void *workspace, size_t workspace_bytes,
+                      aq_stream_t stream);
+aq_status aq_glu_gemm(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      int T, int activation, uint16_t *y, void *workspace, size_t workspace_bytes,
+                      aq_stream_t stream);
+
+/*
+ * Backward pass of the gated block from its input; g and u are computed
+ * again.  With gy = dL/dy [out][T]:
+ *   grad_gate = RN16(gy u act'(g)),  grad_up = RN16(gy act(g))     [out][T]
+ *   grad_x    = RN16(W_g^T (s_g grad_gate) + W_u^T (s_u grad_up))  [in][T], NULL to skip
+ * (of the rounded grad_gate and grad_up; the transposed products as in
+ * aq_input_grad, with one E for both layers).  aq_param_grad(x, grad_gate)
+ * and (x, grad_up) give the scales' and codebooks' gradients.  1 <= T <=
+ * 2^22.  Deterministic.  The outputs overlap no input and not
+ * one another.
+ */
+size_t aq_glu_grad_workspace_bytes(const aq_layer_desc *desc, int T);
+aq_status aq_glu_grad(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,
+                      const uint16_t *gy, int T, int activation, uint16_t *grad_gate, uint16_t *grad_up,
+                      uint16_t *grad_x, void *workspace, size_t workspace_bytes, aq_stream_t stream);
+
+/*
  * Measurement aid, not part of the product path: the codeword-read ceiling
  * of the 1x16 decode-time product.  A 1x16 layer decodes each code by
  * reading its 16-byte codeword from the 1 MiB codebook (the paper's 1x16
