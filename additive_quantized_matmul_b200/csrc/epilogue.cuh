@@ -7,6 +7,8 @@
 // the binary16 results' 2^-11).
 #pragma once
 
+#include <type_traits>
+
 #include "aq_common.cuh"
 
 namespace aqk {
@@ -54,6 +56,39 @@ __device__ __forceinline__ float act_value_slope(int act, float v, float &slope)
         return v * p;
     }
     default: slope = 1.f; return v;
+    }
+}
+
+// v[i] = act(v[i]), with one branch on the activation for all of them.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N])
+{
+    auto all = [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = act_value(decltype(kind)::value, v[i]);
+    };
+    switch (act) {
+    case AQ_ACT_RELU: all(std::integral_constant<int, AQ_ACT_RELU>{}); break;
+    case AQ_ACT_GELU: all(std::integral_constant<int, AQ_ACT_GELU>{}); break;
+    case AQ_ACT_GELU_TANH: all(std::integral_constant<int, AQ_ACT_GELU_TANH>{}); break;
+    case AQ_ACT_SILU: all(std::integral_constant<int, AQ_ACT_SILU>{}); break;
+    }
+}
+
+// v[i] = act(v[i]) and d[i] = act'(v[i]), likewise.
+template <int N>
+__device__ __forceinline__ void act_values_slopes(int act, float (&v)[N], float (&d)[N])
+{
+    auto all = [&](auto kind) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = act_value_slope(decltype(kind)::value, v[i], d[i]);
+    };
+    switch (act) {
+    case AQ_ACT_RELU: all(std::integral_constant<int, AQ_ACT_RELU>{}); break;
+    case AQ_ACT_GELU: all(std::integral_constant<int, AQ_ACT_GELU>{}); break;
+    case AQ_ACT_GELU_TANH: all(std::integral_constant<int, AQ_ACT_GELU_TANH>{}); break;
+    case AQ_ACT_SILU: all(std::integral_constant<int, AQ_ACT_SILU>{}); break;
+    default: all(std::integral_constant<int, AQ_ACT_NONE>{}); break;
     }
 }
 

@@ -1,0 +1,54 @@
+// Input gradient of a quantised layer, gx = W^T (s gy), and of the gated
+// block's two layers at once: the transposed product on the warp-specialised
+// kernel of gemm_ws.cuh (BackOp).
+//
+// A CTA takes 128 input features and 256 or 512 tokens and walks the layer's
+// rows, 64 a stage: the codewords of 8 rows x 16 groups are scaled and laid
+// along M (MN-major A), gy rows come by TMA.  Two layers follow one another
+// in the same accumulator.
+#include "gemm_ws.cuh"
+#include "layer_ops.cuh"
+
+namespace aqh {
+using namespace aqk;
+
+static GemmPlan plan_back(const Geom &g, int layers, int T)
+{
+    return plan_ws(ws_mtiles<BackOp>(g), layers * ws_layer_stages<BackOp>(g), T, ws_max_bn<BackOp>(g));
+}
+
+size_t back_plan_bytes(const Geom &g, int layers, int T) { return plan_back(g, layers, T).ws_bytes; }
+
+cudaError_t launch_back(const Geom &g, int layers, const LayerWeights &w0, const uint16_t *g0, const LayerWeights &w1,
+                        const uint16_t *g1, int T, uint16_t *gx, void *ws, cudaStream_t s)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    TensorMaps<2> maps;
+    const int pitch = padded_tokens(T);
+    if (!token_map(encode, &maps.m[0], g0, g.out, T, pitch) ||
+        !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch))
+        return cudaErrorInvalidValue;
+    const BackOp op{{w0, layers > 1 ? w1 : w0}, layers, gx};
+    return launch_ws(g, plan_back(g, layers, T), maps, op, T, ws, s, true);
+}
+
+size_t input_grad_workspace_bytes(const Geom &g, int T)
+{
+    const size_t plan = back_plan_bytes(g, 1, T);
+    return T % 8 ? align_up(plan) + padded_bytes(g.out, T) : plan;
+}
+
+cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16_t *gy, int T, uint16_t *gx, void *ws,
+                              cudaStream_t s)
+{
+    if (T % 8) {
+        uint16_t *pad = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(ws) + align_up(back_plan_bytes(g, 1, T)));
+        const cudaError_t e = pad_rows(gy, g.out, T, pad, s);
+        if (e != cudaSuccess) return e;
+        gy = pad;
+    }
+    return launch_back(g, 1, w, gy, w, nullptr, T, gx, ws, s);
+}
+
+}  // namespace aqh
