@@ -175,6 +175,30 @@ def test_residual_in_place_and_unit_scales(K, B, n):
     lr.check(half(y, 200, n), lr.fused(c.refs[0], x, "none", None, r), "in place")
 
 
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8), (8, 8)])
+@pytest.mark.parametrize("n", [1, 2, 8, 40])
+def test_scales_and_bias_at_any_even_address(K, B, n):
+    c = Case(520, 1032, K, B, 14, layers=2)
+    x, b, gy = acts(1032, n, 1), acts(520, 1, 2).ravel(), acts(520, n, 3)
+
+    def odd(t):
+        full = torch.zeros(t.numel() + 8, dtype=torch.int16, device="cuda")
+        full[3:3 + t.numel()] = t.view(torch.int16)
+        return full[3:3 + t.numel()]
+
+    c.scales = [odd(s) for s in c.scales]
+    c.weights = [aq.Weights.make(d.packed, k, s) for d, k, s in zip(c.dls, c.books, c.scales)]
+    full, y = guarded(520 * n)
+    ws = workspace(max(aq.aq_gemm_fused_workspace_bytes(c.desc, n), aq.aq_gemv_workspace_bytes(c.desc, min(n, 16))))
+    (aq.aq_gemm_fused if n > 16 else aq.aq_gemv_fused)(*c.w(), fenced(x), n, y, ws, activation=4,
+                                                       bias=odd(fenced(b)))
+    torch.cuda.synchronize()
+    assert guards_intact(full)
+    lr.check(half(y, 520, n), lr.fused(c.refs[0], x, "silu", b), "fused")
+    lr.check(c.glu(x, "silu"), lr.glu(*c.refs, x, "silu"), "glu")
+    lr.check(c.input_grad(gy), c.refs[0].back(gy), "input grad")
+
+
 @pytest.mark.parametrize("K,B", SCHEMES)
 @pytest.mark.parametrize("out,inp", SHAPES + [(1000, 2056)])
 @pytest.mark.parametrize("n", [1, 2, 3, 8, 16])
