@@ -2,9 +2,9 @@
 // functions, their slopes, and the host declarations of the layer operators.
 //
 // All of it is evaluated in fp32 on fp32 sums; the results are rounded once,
-// where they are written.  The exponential is the fast one (ex2.approx,
-// relative error about 2^-22 per unit of its argument's magnitude, far below
-// the binary16 results' 2^-11).
+// where they are written.  Exponential and reciprocal are the approximate
+// instructions (relative errors about 2^-22), far below the binary16
+// results' 2^-11.
 #pragma once
 
 #include <type_traits>
@@ -13,83 +13,81 @@
 
 namespace aqk {
 
-constexpr float kSqrt2OverPi = 0.7978845608028654f;
-constexpr float kSqrtHalf = 0.7071067811865476f;
-constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+// Activations by family, so that an epilogue chooses its code once and not
+// per element: SiLU and the tanh form of GELU are both v p with p the
+// logistic function of v (k1 + k2 v^2) -- (1 + tanh t) / 2 = logistic(2 t),
+// which loses no bits where tanh is near -1 -- and differ in k1, k2 alone.
+constexpr int kActLinear = 0;    // none, ReLU
+constexpr int kActLogistic = 1;  // SiLU, GELU (tanh)
+constexpr int kActErf = 2;       // GELU
 
-// 1 / (1 + e^-v): 0 at -infinity (e^-v is infinite), 1 at infinity.
-__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+struct ActParams {
+    bool relu;
+    float k1, k2;
+};
 
-// The tanh form of GELU is v * logistic(2 t) with this t: (1 + tanh t) / 2 =
-// logistic(2 t), which loses no bits where tanh is near -1.
-__device__ __forceinline__ float gelu_tanh_arg(float v) { return 2.f * kSqrt2OverPi * fmaf(0.044715f * v * v, v, v); }
-
-__device__ __forceinline__ float act_value(int act, float v)
+__host__ __device__ __forceinline__ constexpr int act_family(int act)
 {
-    switch (act) {
-    case AQ_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays one
-    case AQ_ACT_GELU: return v * 0.5f * erfcf(-v * kSqrtHalf);
-    case AQ_ACT_GELU_TANH: return v * logistic(gelu_tanh_arg(v));
-    case AQ_ACT_SILU: return v * logistic(v);
-    default: return v;
-    }
+    return act == AQ_ACT_GELU ? kActErf : act >= AQ_ACT_GELU_TANH ? kActLogistic : kActLinear;
 }
 
-// act(v), and its derivative in `slope`.
-__device__ __forceinline__ float act_value_slope(int act, float v, float &slope)
+__device__ __forceinline__ ActParams act_params(int act)
 {
-    switch (act) {
-    case AQ_ACT_RELU: slope = v > 0.f ? 1.f : 0.f; return v < 0.f ? 0.f : v;
-    case AQ_ACT_GELU: {
+    const bool tanh_form = act == AQ_ACT_GELU_TANH;  // 2 sqrt(2 / pi) (1 + 0.044715 v^2)
+    return ActParams{act == AQ_ACT_RELU, tanh_form ? 1.5957691216057308f : 1.f, tanh_form ? 0.0713548162726009f : 0.f};
+}
+
+// act(v) of a family, and its derivative.
+template <int F>
+__device__ __forceinline__ float act_value(const ActParams &k, float v, float &slope)
+{
+    if constexpr (F == kActLinear) {
+        slope = (k.relu && !(v > 0.f)) ? 0.f : 1.f;
+        return (k.relu && v < 0.f) ? 0.f : v;  // a NaN stays one
+    } else if constexpr (F == kActLogistic) {
+        constexpr float kLog2E = 1.4426950408889634f;
+        const float v2 = v * v;
+        float e, p;
+        // 1 / (1 + 2^(-log2(e) a)): 0 where the power is infinite
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2E * v * fmaf(k.k2, v2, k.k1)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+        const float y = v * p;
+        slope = fmaf(y * (1.f - p), fmaf(3.f * k.k2, v2, k.k1), p);
+        return y;
+    } else {
+        constexpr float kSqrtHalf = 0.7071067811865476f, kInvSqrt2Pi = 0.3989422804014327f;
         const float cdf = 0.5f * erfcf(-v * kSqrtHalf);
         slope = fmaf(v * kInvSqrt2Pi, __expf(-0.5f * v * v), cdf);
         return v * cdf;
     }
-    case AQ_ACT_GELU_TANH: {
-        const float p = logistic(gelu_tanh_arg(v));
-        slope = fmaf(2.f * v * p * (1.f - p), kSqrt2OverPi * fmaf(3.f * 0.044715f * v, v, 1.f), p);
-        return v * p;
-    }
-    case AQ_ACT_SILU: {
-        const float p = logistic(v);
-        slope = fmaf(v * p, 1.f - p, p);
-        return v * p;
-    }
-    default: slope = 1.f; return v;
+}
+template <int F>
+__device__ __forceinline__ float act_value(const ActParams &k, float v)
+{
+    float unused;
+    return act_value<F>(k, v, unused);
+}
+
+// f(std::integral_constant<int, family>) for an activation.
+template <class F>
+__device__ __forceinline__ void with_act_family(int act, F &&f)
+{
+    switch (act_family(act)) {
+    case kActLinear: f(std::integral_constant<int, kActLinear>{}); break;
+    case kActLogistic: f(std::integral_constant<int, kActLogistic>{}); break;
+    default: f(std::integral_constant<int, kActErf>{}); break;
     }
 }
 
-// v[i] = act(v[i]), with one branch on the activation for all of them.
+// v[i] = act(v[i]).
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&v)[N])
 {
-    auto all = [&](auto kind) {
+    const ActParams k = act_params(act);
+    with_act_family(act, [&](auto family) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = act_value(decltype(kind)::value, v[i]);
-    };
-    switch (act) {
-    case AQ_ACT_RELU: all(std::integral_constant<int, AQ_ACT_RELU>{}); break;
-    case AQ_ACT_GELU: all(std::integral_constant<int, AQ_ACT_GELU>{}); break;
-    case AQ_ACT_GELU_TANH: all(std::integral_constant<int, AQ_ACT_GELU_TANH>{}); break;
-    case AQ_ACT_SILU: all(std::integral_constant<int, AQ_ACT_SILU>{}); break;
-    }
-}
-
-// v[i] = act(v[i]) and d[i] = act'(v[i]), likewise.
-template <int N>
-__device__ __forceinline__ void act_values_slopes(int act, float (&v)[N], float (&d)[N])
-{
-    auto all = [&](auto kind) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = act_value_slope(decltype(kind)::value, v[i], d[i]);
-    };
-    switch (act) {
-    case AQ_ACT_RELU: all(std::integral_constant<int, AQ_ACT_RELU>{}); break;
-    case AQ_ACT_GELU: all(std::integral_constant<int, AQ_ACT_GELU>{}); break;
-    case AQ_ACT_GELU_TANH: all(std::integral_constant<int, AQ_ACT_GELU_TANH>{}); break;
-    case AQ_ACT_SILU: all(std::integral_constant<int, AQ_ACT_SILU>{}); break;
-    default: all(std::integral_constant<int, AQ_ACT_NONE>{}); break;
-    }
+        for (int i = 0; i < N; ++i) v[i] = act_value<decltype(family)::value>(k, v[i]);
+    });
 }
 
 __device__ __forceinline__ float half_bits_to_float(uint16_t h) { return __half2float(__ushort_as_half(h)); }

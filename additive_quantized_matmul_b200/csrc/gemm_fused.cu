@@ -6,8 +6,7 @@
 //
 // All run on the warp-specialised kernel of gemm_ws.cuh.  TMA needs rows of
 // 16-byte multiples; for T not a multiple of 8 the activations are first
-// copied to rows of T rounded up to 8 in the workspace, and the kernel's own
-// reads and writes of ragged rows pass through shared memory.
+// copied to rows of T rounded up to 8 in the workspace.
 #include "gemm_ws.cuh"
 #include "layer_ops.cuh"
 
@@ -87,7 +86,7 @@ template <class Op>
 Layout layout_of(const Geom &g, int T)
 {
     Layout l;
-    l.p = plan_ws(ws_mtiles<Op>(g), ws_layer_stages<Op>(g), T, ws_max_bn<Op>(g));
+    l.p = plan_ws(ws_mtiles<Op>(g), ws_layer_stages<Op>(g), T, ws_max_bn<Op>(g), Op::kPairs);
     l.x_pad = align_up(l.p.ws_bytes);
     l.end = T % 8 ? l.x_pad + padded_bytes(g.in, T) : l.p.ws_bytes;
     return l;
@@ -105,8 +104,9 @@ cudaError_t product(const Geom &g, const Layout &l, const uint16_t *x, int T, co
         if (e != cudaSuccess) return e;
         x = xp;
     }
-    TensorMaps<1> maps;
-    if (!token_map(encode, &maps.m[0], x, g.in, T, padded_tokens(T))) return cudaErrorInvalidValue;
+    TensorMaps<Op::kMaps> maps{};
+    if (!token_map(encode, &maps.m[0], x, g.in, T, padded_tokens(T)) || !io_maps(encode, &maps, op, g, T))
+        return cudaErrorInvalidValue;
     return launch_ws(g, l.p, maps, op, T, ws, s, true);
 }
 
@@ -139,7 +139,7 @@ size_t gemm_fused_workspace_bytes(const Geom &g, int T) { return layout_of<Fused
 cudaError_t launch_gemm_fused(const Geom &g, const LayerWeights &w, const uint16_t *x, int T, const EpilogueArgs &ep,
                               uint16_t *y, void *ws, cudaStream_t s)
 {
-    const FusedOp op{{w}, ep.act, ep.bias, ep.residual, y, false, nullptr, 0, nullptr};
+    const FusedOp op{{w}, ep.act, ep.bias, ep.residual, y, false, nullptr, nullptr};
     return product(g, layout_of<FusedOp>(g, T), x, T, op, reinterpret_cast<char *>(ws), s);
 }
 
@@ -148,7 +148,7 @@ size_t glu_gemm_workspace_bytes(const Geom &g, int T) { return layout_of<GatedOp
 cudaError_t launch_glu_gemm(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x, int T,
                             int act, uint16_t *y, void *ws, cudaStream_t s)
 {
-    const GatedOp op{{gate, up}, act, nullptr, y, nullptr, nullptr, nullptr, 0};
+    const GatedOp op{{gate, up}, act, nullptr, y, nullptr, nullptr, nullptr};
     return product(g, layout_of<GatedOp>(g, T), x, T, op, reinterpret_cast<char *>(ws), s);
 }
 
@@ -165,7 +165,7 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
     char *base = reinterpret_cast<char *>(ws);
     float *sums = grad_bias ? reinterpret_cast<float *>(base + r.sums) : nullptr;
     uint16_t *pad = (T % 8 && grad_x) ? reinterpret_cast<uint16_t *>(base + r.pad0) : nullptr;
-    const FusedOp op{{w}, ep.act, ep.bias, gy, grad_z, true, pad, padded_tokens(T), sums};
+    const FusedOp op{{w}, ep.act, ep.bias, gy, grad_z, true, pad, sums};
     cudaError_t e = product(g, r.l, x, T, op, base, s);
     if (e == cudaSuccess && grad_bias)
         e = launch_programmatic(bias_grad_kernel, dim3((g.out + 31) / 32), dim3(256), s, (const float *)sums,
@@ -188,7 +188,7 @@ cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const Layer
     const bool pad = T % 8 && grad_x;
     uint16_t *p0 = pad ? reinterpret_cast<uint16_t *>(base + r.pad0) : nullptr;
     uint16_t *p1 = pad ? reinterpret_cast<uint16_t *>(base + r.pad1) : nullptr;
-    const GatedOp op{{gate, up}, act, gy, grad_gate, grad_up, p0, p1, padded_tokens(T)};
+    const GatedOp op{{gate, up}, act, gy, grad_gate, grad_up, p0, p1};
     const cudaError_t e = product(g, r.l, x, T, op, base, s);
     if (e != cudaSuccess || !grad_x) return e;
     return launch_back(g, 2, gate, pad ? p0 : grad_gate, up, pad ? p1 : grad_up, T, grad_x, ws, s);

@@ -63,17 +63,20 @@ constexpr int kTileABytes = kBM * kBK * 2;  // 16 KiB
 // Ring depth: 4 stages of (16 KiB A + 32 KiB B) for BN = 256, 3 when the
 // codebooks take 16 KiB or more of the shared memory (two layers' 2x8, 8x8);
 // 2 stages of (16 + 64 KiB) for BN = 512.  `BB`: bytes of 8-bit codebooks.
-template <class S, int BN, int BB>
-constexpr int kWsStagesOf = (BN == 512) ? 2 : (BB > 8192 || (S::K == 1 && S::B == 16)) ? 3 : 4;
+// `Pair`: a CTA pair, each CTA holding half of every X tile (32 KiB a stage).
+template <class S, int BN, int BB, bool Pair>
+constexpr int kWsStagesOf = Pair ? 4 : (BN == 512) ? 2 : (BB > 8192 || (S::K == 1 && S::B == 16)) ? 3 : 4;
 // The W (decoded) tiles have a ring of their own, 5 deep (4 with the 32 KiB
 // of 8x8 codebooks): with 512-token X tiles taking 64 KiB a stage, a shared
 // ring would be 2 deep.  The 1x16 decoders (two groups of 128 threads, two
 // of each group's stages in flight: about 4000 codeword reads per CTA) need
 // the depth; at 256-token tiles 1x16 trades an X stage for two W stages
-// (6 W, 3 X).
-template <class S, int BN, int BB>
-constexpr int kWsAStagesOf = (BN == 512) ? ((BB > 16384) ? 4 : 5)
-                                         : ((S::K == 1 && S::B == 16) ? 6 : kWsStagesOf<S, BN, BB>);
+// (6 W, 3 X).  Pairs leave 96 KiB for W tiles and codebooks.
+template <class S, int BN, int BB, bool Pair>
+constexpr int kWsAStagesOf = (Pair && BB == 0)        ? 6
+                             : (BN == 512)              ? ((BB > 16384) ? 4 : 5)
+                             : (S::K == 1 && S::B == 16) ? 6
+                                                         : kWsStagesOf<S, BN, BB, Pair>;
 // Decoder groups of 4 warps taking alternate stages: one CTA per SM (the X
 // tiles fill its shared memory), so the decode rate per SM is that of its
 // decoders; with one or two codebooks two groups run (twice the 1x16
@@ -89,6 +92,10 @@ constexpr int kWsLag = 2;                     // cp.async stages in flight per d
 // Layers whose 8-bit codebooks a CTA keeps in shared memory.
 template <class S, class Op>
 constexpr int kWsBookBytes = S::kSmemBookBytes * Op::kLayers;
+
+// Boxes of an operator's input in a tile.
+template <class Op, int BN>
+constexpr int kInBoxes = Op::kStaged ? BN / 64 * 4 : 0;
 
 template <int N>
 struct TensorMaps {
@@ -107,112 +114,6 @@ struct TailMap {
     int per;   // 64-feature stages per split
 };
 
-// ---- rows of binary16 arrays, 16 tokens of R consecutive rows per warp --------
-//
-// R = 32: lane l has all 16 tokens of row l; R = 16: lane l has tokens
-// 8 (l / 16) .. + 7 of row l % 16.  With T a multiple of 8 the lane reads and
-// writes its 16-byte pieces directly.  Otherwise rows start at any even
-// address: the block passes through a per-warp kilobyte of shared memory so
-// that each access covers 32 consecutive bytes of a row (one row per lane
-// would touch a sector for every 2-byte element).  `load` requests a block,
-// `settle` later brings what arrived into the lane's own pieces.
-template <int R>
-struct RowBlock {
-    static constexpr int kPieces = R / 16;  // 16-byte pieces per lane
-    uint4 p[kPieces];
-};
-
-template <int R>
-struct RowIO {
-    int T, row0, row_end;  // tokens (row pitch), the warp's first row, one past the array's last
-    uint8_t *scratch;      // 1 KiB per warp
-    bool vec;              // T % 8 == 0
-
-    __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
-    __device__ __forceinline__ int row() const { return row0 + (R == 32 ? lane() : (lane() & 15)); }
-    __device__ __forceinline__ int first() const { return R == 32 ? 0 : 8 * (lane() >> 4); }  // lane's first token
-
-    // Tokens gn .. gn + 15 (zeros past T or the last row), not yet settled:
-    // element lane + 32 i of the block in half-word i when T is ragged.
-    __device__ __forceinline__ RowBlock<R> load(const uint16_t *base, int gn) const
-    {
-        RowBlock<R> b;
-#pragma unroll
-        for (int i = 0; i < b.kPieces; ++i) b.p[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (vec) {
-            if (row() < row_end) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(base + (size_t)row() * T + gn + first());
-#pragma unroll
-                for (int i = 0; i < b.kPieces; ++i)
-                    if (gn + first() + 8 * i < T) b.p[i] = __ldcg(src + i);
-            }
-        } else {
-            uint32_t h[R / 2];
-            const int r = row0 + (lane() >> 4), c = gn + (lane() & 15);  // rows r, r + 2, ...
-            const uint16_t *src = base + (size_t)r * T + c;
-#pragma unroll
-            for (int i = 0; i < R / 2; ++i, src += 2 * (size_t)T)
-                h[i] = (r + 2 * i < row_end && c < T) ? (uint32_t)__ldcg(src) : 0u;
-#pragma unroll
-            for (int i = 0; i < b.kPieces; ++i)
-                b.p[i] = make_uint4(h[8 * i] | (h[8 * i + 1] << 16), h[8 * i + 2] | (h[8 * i + 3] << 16),
-                                    h[8 * i + 4] | (h[8 * i + 5] << 16), h[8 * i + 6] | (h[8 * i + 7] << 16));
-        }
-        return b;
-    }
-
-    __device__ __forceinline__ RowBlock<R> settle(RowBlock<R> b) const
-    {
-        if (!vec) {
-            uint16_t *sh = reinterpret_cast<uint16_t *>(scratch);
-#pragma unroll
-            for (int i = 0; i < R / 2; ++i)
-                sh[lane() + 32 * i] = (uint16_t)(u4_at(b.p[i / 8], (i % 8) / 2) >> (16 * (i & 1)));
-            __syncwarp();
-            const uint4 *mine = reinterpret_cast<const uint4 *>(sh + (row() - row0) * 16 + first());
-#pragma unroll
-            for (int i = 0; i < b.kPieces; ++i) b.p[i] = mine[i];
-            __syncwarp();
-        }
-        return b;
-    }
-
-    __device__ __forceinline__ void put(uint16_t *base, int gn, const RowBlock<R> &b) const
-    {
-        if (vec) {
-            if (row() < row_end) {
-                uint4 *dst = reinterpret_cast<uint4 *>(base + (size_t)row() * T + gn + first());
-#pragma unroll
-                for (int i = 0; i < b.kPieces; ++i)
-                    if (gn + first() + 8 * i < T) dst[i] = b.p[i];
-            }
-        } else {
-            uint16_t *sh = reinterpret_cast<uint16_t *>(scratch);
-            uint4 *mine = reinterpret_cast<uint4 *>(sh + (row() - row0) * 16 + first());
-#pragma unroll
-            for (int i = 0; i < b.kPieces; ++i) mine[i] = b.p[i];
-            __syncwarp();
-            const int r = row0 + (lane() >> 4), c = gn + (lane() & 15);
-            uint16_t *dst = base + (size_t)r * T + c;
-#pragma unroll
-            for (int i = 0; i < R / 2; ++i, dst += 2 * (size_t)T)
-                if (r + 2 * i < row_end && c < T) *dst = sh[lane() + 32 * i];
-            __syncwarp();
-        }
-    }
-
-    // The same block into an array whose rows are `pitch` (T rounded up to 8) apart.
-    __device__ __forceinline__ void put_padded(uint16_t *base, int pitch, int gn, const RowBlock<R> &b) const
-    {
-        if (row() < row_end) {
-            uint4 *dst = reinterpret_cast<uint4 *>(base + (size_t)row() * pitch + gn + first());
-#pragma unroll
-            for (int i = 0; i < b.kPieces; ++i)
-                if (gn + first() + 8 * i < pitch) dst[i] = b.p[i];
-        }
-    }
-};
-
 __device__ __forceinline__ uint4 round_h8(const float *v)
 {
     return make_uint4(f2h2(v[0], v[1]), f2h2(v[2], v[3]), f2h2(v[4], v[5]), f2h2(v[6], v[7]));
@@ -227,209 +128,199 @@ __device__ __forceinline__ void widen_h8(uint4 p, float *v)
     f = h2f2(p.w), v[6] = f.x, v[7] = f.y;
 }
 
-// Where a tile's sums are written: the tile, its tokens and the epilogue
-// warp's scratch.
+// Where a tile's sums are written.
 struct TileOut {
     int mt, n0, T;
-    uint8_t *scratch;  // this warp's kilobyte of the (idle) W ring
-    float factor;      // kTransposed: 2^E
+    float factor;  // kTransposed: 2^E
 };
 
 // ---- operators ----------------------------------------------------------------
+//
+// PlainOp stores its rows straight from registers.  The others (kStaged) pass
+// them through shared memory: `kRows` consecutive rows of the output per TMEM
+// lane quarter, from row0(); of 16 accumulator columns (tokens gn ..) a lane
+// turns its share into kPieces 16-byte pieces of its output row (two for 32
+// rows: all 16 tokens; one for 16 rows: tokens 8 (lane / 16) ..), reading the
+// matching pieces of its own input (residual or gradient) if it has one.
+// io() are its arrays: 0 the input, 1 and 2 the outputs, 3 and 4 second
+// copies of them with rows padded to a multiple of 8 tokens; their tensor
+// maps follow the activations' in the kernel's parameters.
 
 // y = RN16(s (W x)); T % 8 == 0.
 struct PlainOp {
-    static constexpr bool kGated = false, kTransposed = false;
-    static constexpr int kLayers = 1, kMaps = 1, kRows = 32, kAhead = 4;
+    static constexpr bool kGated = false, kTransposed = false, kStaged = false;
+    static constexpr int kLayers = 1, kMaps = 1, kXMaps = 1, kAhead = 4;
+    static constexpr bool kPairs = false;
     LayerWeights w[1];
     uint16_t *y;
-
-    struct Row {
-        RowIO<32> io;
-        float sc;
-    };
-    __device__ __forceinline__ Row row(const Geom &L, const TileOut &o) const
-    {
-        Row r;
-        r.io = RowIO<32>{o.T, o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32, L.out, o.scratch, true};
-        const int i = r.io.row();
-        r.sc = (i < L.out && w[0].scales) ? half_bits_to_float(w[0].scales[i]) : 1.f;
-        return r;
-    }
-    __device__ __forceinline__ RowBlock<32> input(const Row &, int) const { return RowBlock<32>{}; }
-    __device__ __forceinline__ void store(const Row &r, int gn, float (&v)[16], const RowBlock<32> &) const
-    {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] *= r.sc;
-        RowBlock<32> b;
-        b.p[0] = round_h8(v);
-        b.p[1] = round_h8(v + 8);
-        r.io.put(y, gn, b);
-    }
 };
 
 // y = RN16(act(s (W x) + bias) + residual), or, with gy: grad_z = RN16(gy
 // act'(z)) and the sums of gy act'(z) over each block of 16 tokens.
 struct FusedOp {
-    static constexpr bool kGated = false, kTransposed = false;
-    static constexpr int kLayers = 1, kMaps = 1, kRows = 32, kAhead = 2;
+    static constexpr bool kGated = false, kTransposed = false, kStaged = true;
+    static constexpr int kLayers = 1, kXMaps = 1, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
+    static constexpr int kMaps = kXMaps + 5;
+    static constexpr bool kPairs = true;
     LayerWeights w[1];
     int act;
     const uint16_t *bias;  // or null
     const uint16_t *in;    // residual, or gy (grad); or null
     uint16_t *out;         // y, or grad_z
     bool grad;
-    uint16_t *padded;      // grad, ragged T: a second copy of grad_z, rows `pitch` apart
-    int pitch;
+    uint16_t *padded;      // grad, ragged T: a second copy of grad_z
     float *sums;           // grad: [blocks of 16 tokens][out], or null
 
     struct Row {
-        RowIO<32> io;
         float sc, b;
     };
+    __host__ __device__ const uint16_t *io(int i) const
+    {
+        return i == 0 ? in : i == 1 ? out : i == 3 ? padded : nullptr;
+    }
+    __device__ __forceinline__ int row0(const TileOut &o) const { return o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32; }
+    __host__ __device__ int rows(const Geom &L) const { return L.out; }
     __device__ __forceinline__ Row row(const Geom &L, const TileOut &o) const
     {
-        Row r;
-        r.io = RowIO<32>{o.T, o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32, L.out, o.scratch, (o.T & 7) == 0};
-        const int i = r.io.row();
-        r.sc = (i < L.out && w[0].scales) ? half_bits_to_float(w[0].scales[i]) : 1.f;
-        r.b = (i < L.out && bias) ? half_bits_to_float(bias[i]) : 0.f;
-        return r;
+        const int i = row0(o) + (int)(threadIdx.x & 31);
+        return Row{(i < L.out && w[0].scales) ? half_bits_to_float(w[0].scales[i]) : 1.f,
+                   (i < L.out && bias) ? half_bits_to_float(bias[i]) : 0.f};
     }
-    __device__ __forceinline__ RowBlock<32> input(const Row &r, int gn) const
+    template <class F>
+    __device__ __forceinline__ void dispatch(F &&f) const
     {
-        return in ? r.io.load(in, gn) : RowBlock<32>{};
+        with_act_family(act, [&](auto family) {
+            if (grad) f(family, std::true_type{});
+            else f(family, std::false_type{});
+        });
     }
-    __device__ __forceinline__ void store(const Row &r, int gn, float (&v)[16], const RowBlock<32> &raw) const
+    template <int Family, bool Grad>
+    __device__ __forceinline__ void apply(const Geom &L, const TileOut &o, const ActParams &k, const Row &r, int gn,
+                                          float (&v)[16], const uint4 (&x)[2], uint4 (&y0)[2], uint4 (&)[2]) const
     {
-        RowBlock<32> x{}, b;
-        if (in) x = r.io.settle(raw);
         float sum = 0.f;
-        // eight tokens at a time: sixteen activations in flight would not fit the registers
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
             float a[8], e[8];
+            widen_h8(x[h], e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = fmaf(r.sc, h ? v[j + 8] : v[j], r.b);
-            widen_h8(h ? x.p[1] : x.p[0], e);
-            if (!grad) {
-                act_values(act, a);
-                if (in) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a[j] += e[j];
-                }
-            } else {
-                float slope[8];
-                act_values_slopes(act, a, slope);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    a[j] = e[j] * slope[j];
-                    if (gn + 8 * h + j < r.io.T) sum += a[j];
+            for (int j = 0; j < 8; ++j) {
+                const float z = fmaf(r.sc, v[8 * h + j], r.b);
+                if constexpr (Grad) {
+                    float slope;
+                    act_value<Family>(k, z, slope);
+                    a[j] = e[j] * slope;
+                    if (gn + 8 * h + j < o.T) sum += a[j];
+                } else {
+                    a[j] = act_value<Family>(k, z) + e[j];  // no residual: e = -0 changes nothing
                 }
             }
-            if (h) b.p[1] = round_h8(a);
-            else b.p[0] = round_h8(a);
+            y0[h] = round_h8(a);
         }
-        if (sums && r.io.row() < r.io.row_end) sums[(size_t)(gn >> 4) * r.io.row_end + r.io.row()] = sum;
-        r.io.put(out, gn, b);
-        if (padded) r.io.put_padded(padded, pitch, gn, b);
+        if constexpr (Grad) {
+            const int i = row0(o) + (int)(threadIdx.x & 31);
+            if (sums && i < L.out) sums[(size_t)(gn >> 4) * L.out + i] = sum;
+        }
     }
 };
 
 // Gated block: y = RN16(act(g) u), or, with gy, the gradients of g and u.
 struct GatedOp {
-    static constexpr bool kGated = true, kTransposed = false;
-    static constexpr int kLayers = 2, kMaps = 1, kRows = 16, kAhead = 4;
+    static constexpr bool kGated = true, kTransposed = false, kStaged = true;
+    static constexpr int kLayers = 2, kXMaps = 1, kRows = 16, kPieces = 1, kOutputs = 2, kAhead = 4;
+    static constexpr int kMaps = kXMaps + 5;
+    static constexpr bool kPairs = true;
     LayerWeights w[2];  // gate, up
     int act;
     const uint16_t *gy;      // or null: forward
     uint16_t *out0, *out1;   // y, -; or grad_gate, grad_up
-    uint16_t *padded0, *padded1;  // grad, ragged T: second copies, rows `pitch` apart
-    int pitch;
+    uint16_t *padded0, *padded1;  // grad, ragged T: second copies
 
     struct Row {
-        RowIO<16> io;
         float sc;
     };
+    __host__ __device__ const uint16_t *io(int i) const
+    {
+        return i == 0 ? gy : i == 1 ? out0 : i == 2 ? out1 : i == 3 ? padded0 : padded1;
+    }
+    __device__ __forceinline__ int row0(const TileOut &o) const
+    {
+        return o.mt * (kBM / 2) + (int)((threadIdx.x >> 5) & 3) * 16;
+    }
+    __host__ __device__ int rows(const Geom &L) const { return L.out; }
     __device__ __forceinline__ Row row(const Geom &L, const TileOut &o) const
     {
         // lanes 0-15: gate rows, 16-31: the same rows of up
-        Row r;
-        r.io = RowIO<16>{o.T, o.mt * (kBM / 2) + (int)((threadIdx.x >> 5) & 3) * 16, L.out, o.scratch, (o.T & 7) == 0};
+        const int i = row0(o) + (int)(threadIdx.x & 15);
         const uint16_t *s = (threadIdx.x & 16) ? w[1].scales : w[0].scales;
-        r.sc = (r.io.row() < L.out && s) ? half_bits_to_float(s[r.io.row()]) : 1.f;
-        return r;
-    }
-    __device__ __forceinline__ RowBlock<16> input(const Row &r, int gn) const
-    {
-        return gy ? r.io.load(gy, gn) : RowBlock<16>{};
+        return Row{(i < L.out && s) ? half_bits_to_float(s[i]) : 1.f};
     }
     // Lane l < 16 (gate) gives its tokens 8-15 to lane l + 16 (up) for that
     // lane's tokens 0-7: each then has eight tokens of both projections.
-    __device__ __forceinline__ void store(const Row &r, int gn, float (&v)[16], const RowBlock<16> &raw) const
+    template <class F>
+    __device__ __forceinline__ void dispatch(F &&f) const
+    {
+        with_act_family(act, [&](auto family) {
+            if (gy) f(family, std::true_type{});
+            else f(family, std::false_type{});
+        });
+    }
+    template <int Family, bool Grad>
+    __device__ __forceinline__ void apply(const Geom &, const TileOut &, const ActParams &k, const Row &r, int,
+                                          float (&v)[16], const uint4 (&x)[1], uint4 (&y0)[1], uint4 (&y1)[1]) const
     {
         const bool hi = threadIdx.x & 16;
-        float e[8], a[8], c[8];
-        if (gy) widen_h8(r.io.settle(raw).p[0], e);
+        float a[8], c[8], e[8];
+        if constexpr (Grad) widen_h8(x[0], e);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float lo_v = r.sc * v[j], hi_v = r.sc * v[j + 8];
             const float got = __shfl_xor_sync(0xffffffffu, hi ? lo_v : hi_v, 16);
-            a[j] = hi ? got : lo_v;   // gate
-            c[j] = hi ? hi_v : got;   // up
-        }
-        RowBlock<16> b;
-        if (!gy) {
-            act_values(act, a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] *= c[j];
-            b.p[0] = round_h8(a);
-            r.io.put(out0, gn, b);
-        } else {
-            float slope[8];
-            act_values_slopes(act, a, slope);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = c[j];
-                c[j] = e[j] * a[j];
-                a[j] = e[j] * u * slope[j];
+            const float g = hi ? got : lo_v, u = hi ? hi_v : got;  // gate, up
+            if constexpr (Grad) {
+                float slope;
+                c[j] = e[j] * act_value<Family>(k, g, slope);
+                a[j] = e[j] * u * slope;
+            } else {
+                a[j] = act_value<Family>(k, g) * u;
             }
-            b.p[0] = round_h8(a);
-            r.io.put(out0, gn, b);
-            if (padded0) r.io.put_padded(padded0, pitch, gn, b);
-            b.p[0] = round_h8(c);
-            r.io.put(out1, gn, b);
-            if (padded1) r.io.put_padded(padded1, pitch, gn, b);
         }
+        y0[0] = round_h8(a);
+        if constexpr (Grad) y1[0] = round_h8(c);
     }
 };
 
 // gx = RN16(sum over the layers of W^T (s gy)).
 struct BackOp {
-    static constexpr bool kGated = false, kTransposed = true;
-    static constexpr int kLayers = 2, kMaps = 2, kRows = 32, kAhead = 4;
+    static constexpr bool kGated = false, kTransposed = true, kStaged = true;
+    static constexpr int kLayers = 2, kXMaps = 2, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
+    static constexpr int kMaps = kXMaps + 5;
+    static constexpr bool kPairs = true;
     LayerWeights w[2];
     int layers;  // 1 or 2
     uint16_t *gx;
+    static constexpr int act = AQ_ACT_NONE;
 
     struct Row {
-        RowIO<32> io;
         float sc;
     };
-    __device__ __forceinline__ Row row(const Geom &L, const TileOut &o) const
+    __host__ __device__ const uint16_t *io(int i) const { return i == 1 ? gx : nullptr; }
+    __device__ __forceinline__ int row0(const TileOut &o) const { return o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32; }
+    __host__ __device__ int rows(const Geom &L) const { return L.in; }
+    __device__ __forceinline__ Row row(const Geom &, const TileOut &o) const { return Row{o.factor}; }
+    template <class F>
+    __device__ __forceinline__ void dispatch(F &&f) const
     {
-        return Row{RowIO<32>{o.T, o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32, L.in, o.scratch, (o.T & 7) == 0},
-                   o.factor};
+        f(std::integral_constant<int, kActLinear>{}, std::false_type{});
     }
-    __device__ __forceinline__ RowBlock<32> input(const Row &, int) const { return RowBlock<32>{}; }
-    __device__ __forceinline__ void store(const Row &r, int gn, float (&v)[16], const RowBlock<32> &) const
+    template <int, bool>
+    __device__ __forceinline__ void apply(const Geom &, const TileOut &, const ActParams &, const Row &r, int,
+                                          float (&v)[16], const uint4 (&)[2], uint4 (&y0)[2], uint4 (&)[2]) const
     {
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] *= r.sc;
-        RowBlock<32> b;
-        b.p[0] = round_h8(v);
-        b.p[1] = round_h8(v + 8);
-        r.io.put(gx, gn, b);
+        y0[0] = round_h8(v);
+        y0[1] = round_h8(v + 8);
     }
 };
 
@@ -446,34 +337,6 @@ template <class Op>
 __host__ __device__ __forceinline__ int ws_layer_stages(const Geom &L)
 {
     return ((Op::kTransposed ? L.out : L.in) + kBK - 1) / kBK;
-}
-
-// Runs the operator over this warp's blocks of 16 tokens: columns c, c +
-// step, ... below `end`, the sums of a block from `sums(c, v)`.  The
-// operator's own input of a block is requested two blocks ahead.
-template <class Op, class F>
-__device__ __forceinline__ void finish_blocks(const Op &op, const Geom &L, const TileOut &o, int c, int step, int end,
-                                              F &&sums)
-{
-    const typename Op::Row row = op.row(L, o);
-    end = min(end, o.T - o.n0);
-    RowBlock<Op::kRows> in[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (c + i * step < end) in[i] = op.input(row, o.n0 + c + i * step);
-#pragma unroll 1
-    for (; c < end; c += 2 * step) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int ci = c + i * step;
-            if (ci >= end) break;  // warp-uniform
-            float v[16];
-            sums(ci, v);
-            const RowBlock<Op::kRows> x = in[i];
-            if (ci + 2 * step < end) in[i] = op.input(row, o.n0 + ci + 2 * step);
-            op.store(row, o.n0 + ci, v, x);
-        }
-    }
 }
 
 // Sums of one block of 16 columns over the `ks` splits of a tile, in split
@@ -507,6 +370,177 @@ __device__ __forceinline__ void add_slices(float (&v)[16], const float4 *src, si
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = acc[j];
+}
+
+// The splits of a tile: their slices at this thread's row, and which of them
+// this CTA is (ks = 1: the sums are whole).
+template <int BN>
+struct Splits {
+    const float4 *slices;
+    int ks, z;
+    template <int kAhead>
+    __device__ __forceinline__ void add(int c, float (&v)[16]) const
+    {
+        constexpr size_t kSlice = kBM * BN / 4;  // float4 per slice
+        if (ks > 1) add_slices<kAhead>(v, slices + ((c / 16) * 4) * kBM, kSlice, ks, z);
+    }
+};
+
+// Rows row0 .. row0 + R - 1 (below nrows), tokens gn .. gn + 63 (below T), of
+// a [nrows][T] array to (load) or from a 128-byte-swizzled box: 32 lanes of
+// consecutive tokens an access.
+template <int R, bool kLoad>
+__device__ __forceinline__ void copy_rows(uint16_t *__restrict__ a, int T, int row0, int nrows, int gn, uint8_t *box)
+{
+    const int lane = threadIdx.x & 31;
+    uint16_t *p = a + (size_t)row0 * T + gn + lane;
+    const bool t0 = gn + lane < T, t1 = gn + lane + 32 < T;
+    const int live = min(R, nrows - row0);
+#pragma unroll 8
+    for (int r = 0; r < live; ++r, p += T) {
+        // token t of the row: half-word t % 8 of chunk t / 8
+        uint16_t *s0 = reinterpret_cast<uint16_t *>(box + sw128((uint32_t)r, (uint32_t)lane >> 3)) + (lane & 7);
+        uint16_t *s1 = reinterpret_cast<uint16_t *>(box + sw128((uint32_t)r, (uint32_t)(lane + 32) >> 3)) + (lane & 7);
+        if (kLoad) {
+            const uint16_t h0 = t0 ? __ldcg(p) : (uint16_t)0, h1 = t1 ? __ldcg(p + 32) : (uint16_t)0;
+            *s0 = h0;
+            *s1 = h1;
+        } else {
+            if (t0) p[0] = *s0;
+            if (t1) p[32] = *s1;
+        }
+    }
+}
+
+// A warp's share of the finish: accumulator columns [c, end) of its 32 TMEM
+// lanes at `tq`, 64 at a time, every `step`, as blocks of 16.  The next
+// block's columns are requested before a block is worked on.
+template <class F>
+__device__ __forceinline__ void accumulator_blocks(uint32_t tq, int c, int step, int end, F &&block)
+{
+    uint32_t acc[16];
+    if (c < end) tmem_ld16_start(tq + (uint32_t)c, acc);
+#pragma unroll 1
+    while (c < end) {
+        float v[16];
+        tmem_ld16_wait(acc, v);
+        const int next = ((c + 16) & 63) ? c + 16 : c + 16 - 64 + step;
+        if (next < end) tmem_ld16_start(tq + (uint32_t)next, acc);
+        block(c, v);
+        c = next;
+    }
+}
+
+// Rows straight from registers.
+template <int BN>
+__device__ __forceinline__ void finish_direct(const PlainOp &op, const Geom &L, const TileOut &o, uint32_t tq, int c,
+                                              int step, int end, const Splits<BN> &splits)
+{
+    const int row = o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32 + (int)(threadIdx.x & 31);
+    const float sc = (row < L.out && op.w[0].scales) ? half_bits_to_float(op.w[0].scales[row]) : 1.f;
+    end = min(end, o.T - o.n0);
+#pragma unroll 1
+    for (; c < end; c += step) {
+        float v[16];
+        tmem_ld16(tq + (uint32_t)c, v);
+        splits.template add<PlainOp::kAhead>(c, v);
+        if (row >= L.out) continue;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= sc;
+        uint4 *dst = reinterpret_cast<uint4 *>(op.y + (size_t)row * o.T + o.n0 + c);
+        dst[0] = round_h8(v);
+        if (o.n0 + c + 8 < o.T) dst[1] = round_h8(v + 8);  // T % 8 == 0
+    }
+}
+
+// Rows through shared memory: 64 tokens x kRows rows per warp and step in the
+// layout of a 128-byte-swizzled TMA box, in the ring that the MMAs no longer
+// read.  The input's boxes come by TMA, all requested at once; a lane reads
+// its pieces, writes its results over them, and the box leaves by TMA.  (One
+// row per lane straight to memory would make 32 requests of 32 bytes an
+// instruction: measured 18 to 40 thousand cycles a tile instead of 7 to 12.)
+// With T not a multiple of 8 the rows start at any even address: the warp
+// copies the box's rows itself, 64 consecutive bytes an access.
+// Not inlined: its registers are its own, and the decoders' loop keeps theirs.
+template <int Family, bool Grad, int BN, class Op>
+__device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const TileOut &o, const CUtensorMap *io,
+                                           uint8_t *stage, uint64_t *in_bar, void *ws, uint32_t tq, int c, int step,
+                                           int end, const Splits<BN> &splits)
+{
+    constexpr int R = Op::kRows, P = Op::kPieces;
+    constexpr int kBox = R * 128;  // bytes of a box
+    constexpr bool kTwo = Op::kOutputs > 1 && Grad;
+    constexpr uint32_t kNegZero = 0x80008000u;  // the neutral addend of a missing residual
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+    const int row0 = op.row0(o), nrows = op.rows(L);
+    const typename Op::Row row = op.row(L, o);
+    const ActParams k = act_params(op.act);
+    end = min(end, o.T - o.n0);
+    if (row0 >= nrows || c >= end) return;  // (a pair's second row tile may be empty)
+    const bool vec = (o.T & 7) == 0;
+    const int r_lane = R == 32 ? lane : lane & 15, p_lane = R == 32 ? 0 : lane >> 4;
+    auto box = [&](int cb, int a) { return stage + ((size_t)a * (BN / 64) + cb / 64) * (4 * kBox) + q * kBox; };
+    const uint16_t *in = op.io(0);
+    if (in && vec && lane == 0) {
+        fence_proxy_async_smem();
+        for (int cb = c; cb < end; cb += step) {
+            uint64_t *bar = &in_bar[(cb / 64) * 4 + q];
+            mbar_arrive_expect_tx(bar, kBox);
+            tma_load_2d(smem_u32(box(cb, 0)), &io[0], o.n0 + cb, row0, bar);
+        }
+    }
+    __syncwarp();
+    accumulator_blocks(tq, c, step, end, [&](int cc, float (&v)[16]) {
+        const int cb = cc & ~63, b = (cc & 63) / 16;
+        uint8_t *b0 = box(cb, 0);
+        if (in && b == 0) {
+            if (vec) {
+                if (!mbar_wait_ns(&in_bar[(cb / 64) * 4 + q], 0, kWaitNs)) record_status(ws, AQ_ERR_TIMEOUT);
+            } else {
+                copy_rows<R, true>(const_cast<uint16_t *>(in), o.T, row0, nrows, o.n0 + cb, b0);
+            }
+            __syncwarp();
+        }
+        splits.template add<Op::kAhead>(cc, v);
+        uint4 x[P], y0[P], y1[P];
+        // piece i of the lane: 16-byte chunk 2 b + p_lane + i of its row
+        uint32_t at[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            at[i] = sw128((uint32_t)r_lane, (uint32_t)(2 * b + p_lane + i));
+            x[i] = in ? *reinterpret_cast<const uint4 *>(b0 + at[i]) : make_uint4(kNegZero, kNegZero, kNegZero, kNegZero);
+        }
+        op.template apply<Family, Grad>(L, o, k, row, o.n0 + cc, v, x, y0, y1);
+        uint8_t *b1 = kTwo ? box(cb, 1) : nullptr;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            *reinterpret_cast<uint4 *>(b0 + at[i]) = y0[i];
+            if (kTwo) *reinterpret_cast<uint4 *>(b1 + at[i]) = y1[i];
+        }
+        if (b == 3 || cc + 16 >= end) {  // the box is complete (or the tokens are)
+            if (vec || op.io(3)) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (vec) {
+                        tma_store_2d(&io[1], smem_u32(b0), o.n0 + cb, row0);
+                        if (kTwo) tma_store_2d(&io[2], smem_u32(b1), o.n0 + cb, row0);
+                    } else {
+                        tma_store_2d(&io[3], smem_u32(b0), o.n0 + cb, row0);
+                        if (Op::kOutputs > 1 && op.io(4)) tma_store_2d(&io[4], smem_u32(b1), o.n0 + cb, row0);
+                    }
+                    bulk_commit();
+                }
+            }
+            if (!vec) {
+                __syncwarp();
+                copy_rows<R, false>(const_cast<uint16_t *>(op.io(1)), o.T, row0, nrows, o.n0 + cb, b0);
+                if (kTwo)
+                    copy_rows<R, false>(const_cast<uint16_t *>(op.io(2)), o.T, row0, nrows, o.n0 + cb, b1);
+            }
+        }
+    });
+    bulk_wait_all();  // the boxes have been read and written
 }
 
 // ---- split contractions ---------------------------------------------------------
@@ -578,15 +612,15 @@ __device__ __forceinline__ void decoder_barrier(int threads)
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
 
-template <class S, int BN, class Op>
+template <class S, int BN, class Op, bool Pair>
 __global__ void __launch_bounds__(kWsThreadsOf<S>, 1)
 gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const __grid_constant__ Op op, int T,
                void *ws, GemmSplit sp, int stages_per_split, int cluster_ks, TailMap tm)
 {
     constexpr int BB = kWsBookBytes<S, Op>;
-    constexpr int kWsStages = kWsStagesOf<S, BN, BB>;    // X ring
-    constexpr int kWsAStages = kWsAStagesOf<S, BN, BB>;  // W ring
-    constexpr int kWsTileB = kBK * BN * 2;   // 32 or 64 KiB
+    constexpr int kWsStages = kWsStagesOf<S, BN, BB, Pair>;    // X ring
+    constexpr int kWsAStages = kWsAStagesOf<S, BN, BB, Pair>;  // W ring
+    constexpr int kWsTileB = kBK * BN * 2 / (Pair ? 2 : 1);    // 32 or 64 KiB
     constexpr int kN = BN < 256 ? BN : 256;  // N of one MMA instruction
     constexpr int NG = kWsGroupsOf<S>;       // decoder groups
     constexpr bool kTr = Op::kTransposed;
@@ -600,8 +634,10 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     uint64_t *full_b = full_a + kWsAStages;
     uint64_t *empty = full_b + kWsStages;       // X buffers free
     uint64_t *empty_a = empty + kWsStages;      // W buffers free
-    uint64_t *acc_full = empty_a + kWsAStages;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 1);
+    uint64_t *peer_a = empty_a + kWsAStages;    // pair with asynchronous copies: the odd CTA's W buffer is full
+    uint64_t *acc_full = peer_a + (Pair ? kWsAStages : 0);
+    uint64_t *in_bar = acc_full + 1;            // kStaged: the input's boxes, one per 64 tokens and lane quarter
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_bar + kInBoxes<Op, BN>);
     uint32_t *abort_flag = tmem_slot + 1;
     uint32_t *scale_max = abort_flag + 1;       // kTransposed: largest |s| (binary16 bits)
     uint32_t *last_flag = scale_max + 1;        // the last split of a tail tile
@@ -612,10 +648,12 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     if constexpr (kTr) all_stages *= op.layers;
     // the CTA's tile and split: a 3-D grid (row tile, token tile, split), or
     // the tail mode's 1-D grid
+    // (a pair takes two row tiles, 2 u and 2 u + 1, of which the last may be empty)
+    const int half = Pair ? blockIdx.x & 1 : 0;
     int mt = blockIdx.x, nt = blockIdx.y, z = blockIdx.z, per = stages_per_split, tail_idx = -1;
     if (tm.ks > 0) {
-        const int mtiles = ws_mtiles<Op>(L);
-        int tile = blockIdx.x;
+        const int mtiles = Pair ? (ws_mtiles<Op>(L) + 1) / 2 : ws_mtiles<Op>(L);
+        int tile = Pair ? blockIdx.x >> 1 : blockIdx.x;
         z = 0;
         per = all_stages;
         if (tile >= tm.full) {
@@ -624,8 +662,10 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             z = rr % tm.ks;
             tile = tm.full + tail_idx;
             per = tm.per;
+            if (Pair) tail_idx = 2 * tail_idx + half;  // each CTA has slices and a counter of its own
         }
         mt = tile % mtiles;
+        if (Pair) mt = 2 * mt + half;
         nt = tile / mtiles;
     }
     const int n0 = nt * BN;
@@ -648,25 +688,45 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     }
     if (tid == 0) {
         for (int s = 0; s < kWsAStages; ++s) {
-            mbar_init(&full_a[s], 128);
+            // one arrival per decoder thread; pair: the leader's, one per warp
+            // of both CTAs (asynchronous copies arrive at home, see peer_a)
+            mbar_init(&full_a[s], Pair && !kAsyncWeights ? 8 : 128);
             mbar_init(&empty_a[s], 1);
+            if (Pair && kAsyncWeights) mbar_init(&peer_a[s], 1);
         }
         for (int s = 0; s < kWsStages; ++s) {
             mbar_init(&full_b[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        for (int i = 0; i < kInBoxes<Op, BN>; ++i) mbar_init(&in_bar[i], 1);
         *abort_flag = 0;
         *scale_max = 0;
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc(tmem_slot, BN);
+    if (warp == 0) {
+        if constexpr (Pair) tmem_alloc_pair(tmem_slot, BN);
+        else tmem_alloc(tmem_slot, BN);
+    }
     tc_fence_before();
     __syncthreads();
+    if constexpr (Pair) cluster_sync_all();  // the leader's barriers, before anyone arrives on them
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t leader = Pair ? cluster_ctarank() & ~1u : 0;  // cluster rank
+    const uint16_t pair_mask = (uint16_t)(3u << leader);
     volatile uint32_t *abort_v = abort_flag;
-    TileOut out{mt, n0, T, tileA + (warp >= 2 ? warp - 2 : 0) * 1024, 1.f};
+    // this thread's (Pair: warp's, by one lane) writes of a W stage are visible to the MMAs
+    auto publish = [&](int s) {
+        fence_proxy_async_smem();
+        if constexpr (Pair) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_shared(&full_a[s % kWsAStages], leader));
+        } else {
+            mbar_arrive(&full_a[s % kWsAStages]);
+        }
+    };
+    TileOut out{mt, n0, T, 1.f};
     // programmatic dependent launch: before the wait a thread reads weights
     // only (codes, codebooks); X, y, the scales and the workspace follow it
     grid_launch_dependents();
@@ -682,33 +742,61 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     break;
                 }
                 if (*abort_v) break;
-                mbar_arrive_expect_tx(&full_b[buf], kWsTileB);
+                // pair: both halves complete on the leader's barrier
+                if (!Pair || half == 0) mbar_arrive_expect_tx(&full_b[buf], kWsTileB * (Pair ? 2 : 1));
                 const uint32_t dst = smem_u32(tileB + buf * kWsTileB);
                 int row = (s0 + s) * kBK;
                 const CUtensorMap *map = &maps.m[0];
-                if constexpr (Op::kMaps > 1)
+                if constexpr (Op::kXMaps > 1)
                     if (s0 + s >= layer_stages) {
                         map = &maps.m[1];
                         row -= layer_stages * kBK;
                     }
+                if constexpr (Pair) {
+                    // of each 256 tokens of an MMA this CTA holds 128
+                    const uint32_t bar = map_shared(&full_b[buf], leader);
 #pragma unroll
-                for (int q = 0; q < BN / 64; ++q)
-                    tma_load_2d(dst + q * (kBK * 128), map, n0 + 64 * q, row, &full_b[buf]);
+                    for (int q = 0; q < BN / 128; ++q)
+                        tma_load_2d_pair(dst + q * (kBK * 128), map, n0 + 256 * (q >> 1) + 128 * half + 64 * (q & 1), row,
+                                         bar);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < BN / 64; ++q)
+                        tma_load_2d(dst + q * (kBK * 128), map, n0 + 64 * q, row, &full_b[buf]);
+                }
             }
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            const uint32_t idesc = make_idesc(kBM, kN, true) | (kTr ? 1u << 15 : 0u);  // kTr: A MN-major
+        // first, the tile of the operator's own input (residual, gradient)
+        // into L2, where the epilogue will ask for it
+        const uint16_t *in = nullptr;
+        if constexpr (Op::kStaged) in = op.io(0);
+        if (in) {
+            grid_dependency_wait();
+            const int rows = Op::kGated ? kBM / 2 : kBM;
+            for (int i = lane; i < rows && mt * rows + i < L.out; i += 32) {
+                const uintptr_t p = reinterpret_cast<uintptr_t>(in + (size_t)(mt * rows + i) * T + n0);
+                const uintptr_t e = p + 2 * (size_t)min(BN, T - n0), a = p & ~(uintptr_t)15;
+                if (((e - a) & ~(uintptr_t)15) > 0)
+                    prefetch_l2_bulk(reinterpret_cast<const void *>(a), (uint32_t)((e - a) & ~(uintptr_t)15));
+            }
+            __syncwarp();
+        }
+        if (lane == 0 && half == 0) {  // pair: the leader
+            const uint32_t idesc = make_idesc(Pair ? 2 * kBM : kBM, kN, true) | (kTr ? 1u << 15 : 0u);  // kTr: A MN-major
             int s = 0;
             for (; s < nk; ++s) {
                 const int buf = s % kWsStages, abuf = s % kWsAStages;
-                if (!mbar_wait_ns(&full_a[abuf], (s / kWsAStages) & 1, kWaitNs) ||
-                    !mbar_wait_ns(&full_b[buf], (s / kWsStages) & 1, kWaitNs)) {
+                const uint32_t pa = (s / kWsAStages) & 1, pb = (s / kWsStages) & 1;
+                if (!mbar_wait_ns(&full_a[abuf], pa, kWaitNs) || !mbar_wait_ns(&full_b[buf], pb, kWaitNs)) {
                     *abort_v = 1;
                     break;
                 }
+                if constexpr (Pair && kAsyncWeights)
+                    if (!mbar_wait_ns(&peer_a[abuf], pa, kWaitNs)) *abort_v = 1;
                 if (*abort_v) break;
+                if constexpr (kAsyncWeights) fence_proxy_async_smem();  // the decoders' copies, before the MMAs
                 tc_fence_after();
                 const uint32_t a0 = smem_u32(tileA + abuf * kTileABytes);
                 const uint32_t b0 = smem_u32(tileB + buf * kWsTileB);
@@ -719,15 +807,37 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                                             : smem_desc_sw128(a0 + ks * 32, 16, 1024);
 #pragma unroll
                     for (int h = 0; h < BN / kN; ++h) {
-                        // tokens 256 h .. : four 64-token boxes further on
-                        const uint64_t bd = smem_desc_sw128(b0 + h * (kN / 64) * (kBK * 128) + ks * 2048, kBK * 128, 1024);
-                        mma_f16_ss(tmem + h * kN, ad, bd, idesc, (s > 0 || ks > 0) ? 1u : 0u);
+                        // tokens 256 h .. : four 64-token boxes further on (pair: two, of each CTA)
+                        constexpr int kBoxes = kN / 64 / (Pair ? 2 : 1);
+                        const uint64_t bd = smem_desc_sw128(b0 + h * kBoxes * (kBK * 128) + ks * 2048, kBK * 128, 1024);
+                        const uint32_t acc = (s > 0 || ks > 0) ? 1u : 0u;
+                        if constexpr (Pair) mma_f16_ss_pair(tmem + h * kN, ad, bd, idesc, acc);
+                        else mma_f16_ss(tmem + h * kN, ad, bd, idesc, acc);
                     }
                 }
-                mma_commit(&empty[buf]);     // X buffer free once these MMAs complete
-                mma_commit(&empty_a[abuf]);  // and the W buffer
+                // X buffer free once these MMAs complete, and the W buffer
+                if constexpr (Pair) {
+                    mma_commit_pair(&empty[buf], pair_mask);
+                    mma_commit_pair(&empty_a[abuf], pair_mask);
+                } else {
+                    mma_commit(&empty[buf]);
+                    mma_commit(&empty_a[abuf]);
+                }
             }
-            mma_commit(acc_full);  // completes when every MMA issued above has
+            // completes when every MMA issued above has
+            if constexpr (Pair) mma_commit_pair(acc_full, pair_mask);
+            else mma_commit(acc_full);
+        }
+        if constexpr (Pair && kAsyncWeights) {
+            // the odd CTA's copies have landed: tell the leader
+            if (lane == 0 && half == 1)
+                for (int s = 0; s < nk; ++s) {
+                    const int abuf = s % kWsAStages;
+                    if (!mbar_wait_ns(&full_a[abuf], (s / kWsAStages) & 1, kWaitNs)) *abort_v = 1;
+                    if (*abort_v) break;
+                    fence_proxy_async_smem();
+                    mbar_arrive_cluster(map_shared(&peer_a[abuf], leader));
+                }
         }
     } else {
         // ---------------- decoders ----------------
@@ -762,24 +872,31 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         Chunk<S> code_ring[kCodeAhead];
 #pragma unroll
         for (int q = 0; q < kCodeAhead; ++q) code_ring[q] = fetch(dg + NG * q);
-        // kTransposed: the rows' scales divided by 2^E, one per lane (rows of
-        // the warp's two row tiles), as far ahead as the codes
+        // kTransposed: the rows' scales, one per lane (rows of the warp's two
+        // row tiles), as far ahead as the codes; divided by 2^E where used
         float inv = 1.f;
-        uint32_t scale_ring[kCodeAhead];
-        auto fetch_scale = [&](int s) -> uint32_t {
+        uint16_t scale_ring[kCodeAhead];
+        auto fetch_scale = [&](int s) -> uint16_t {
             const int l = layer_of(s), o = (tile_of(s) - (rt_l & 1)) * 8 + (lane & 15);
-            if (s >= nk || o >= L.out) return 0u;  // rows past the layer weigh nothing
+            if (s >= nk || o >= L.out) return (uint16_t)0;  // rows past the layer weigh nothing
             const uint16_t *sc = op.w[l].scales;
-            return (uint32_t)float_to_half_bits(sc ? half_bits_to_float(__ldg(sc + o)) * inv : inv);
+            return sc ? __ldg(sc + o) : (uint16_t)0x3c00;
         };
-        uint4 ahead[8];  // kTransposed, one 16-bit codebook: the next stage's codewords
+        // kTransposed, one 16-bit codebook: the codewords of the next two own
+        // stages (4096 reads in flight per SM)
         constexpr bool kGatherAhead = kTr && S::K == 1 && S::B == 16;
+        uint4 ahead[2][8];
         if constexpr (kTr) {
             if constexpr (kGatherAhead) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) ahead[r] = ldg_nc_v4(op.w[layer_of(dg)].cb + code_ring[0].code(r, 0));
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        ahead[q][r] = ldg_nc_v4(op.w[layer_of(dg + NG * q)].cb + code_ring[q].code(r, 0));
             }
             grid_dependency_wait();  // the scales
+#pragma unroll
+            for (int q = 0; q < kCodeAhead; ++q) scale_ring[q] = fetch_scale(dg + NG * q);
             uint32_t m = 0;
             for (int l = 0; l < op.layers; ++l)
                 m = max(m, op.w[l].scales ? absmax_share(op.w[l].scales, L.out, tid - 64, 128 * NG) : 0x3c00u);
@@ -794,56 +911,30 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             else if (m) e = ilogbf(half_bits_to_float((uint16_t)m)) + 1;
             inv = ldexpf(1.f, -e);
             out.factor = ldexpf(1.f, e);
-#pragma unroll
-            for (int q = 0; q < kCodeAhead; ++q) scale_ring[q] = fetch_scale(dg + NG * q);
         }
-        // copies of kLag stages stay in flight; a stage is published kLag
-        // iterations after it is issued, so kLag must stay below the ring
-        // depth (the decoder waits for the MMAs of stage s - depth first)
-        // (with NG groups a lag of kLag own stages spans NG kLag stages of the ring)
-        constexpr int kLag = !kAsyncWeights ? 0 : kWsLag;
-        static_assert(NG * kLag < kWsAStages || !kAsyncWeights, "copy lag must leave the MMAs a stage of slack");
         bool ok = true;
-        int published = 0;  // own stages below this have been arrived on full_a[]
         // unrolled by the ring depth so every ring index is static
-        for (int k0 = 0; ok && k0 < nown + kLag; k0 += kCodeAhead) {
+        for (int k0 = 0; ok && k0 < nown; k0 += kCodeAhead) {
 #pragma unroll
             for (int u = 0; u < kCodeAhead; ++u) {
                 const int k = k0 + u, s = dg + NG * k;  // own stage, stage
-                if (k >= nown + kLag) break;
-                if (k < nown) {
+                if (k >= nown) break;
+                {
                     const int buf = s % kWsAStages;
-                    // the buffer is free once the MMAs of stage s - depth
-                    // completed; before blocking on it, publish every stage
-                    // this thread has issued (the MMAs may need them first)
-                    if (s >= kWsAStages) {
-                        const uint32_t par = ((s / kWsAStages) - 1) & 1;
-                        if (!mbar_test_wait(&empty_a[buf], par)) {
-                            if constexpr (kAsyncWeights) {
-                                cp_async_wait<0>();
-                                fence_proxy_async_smem();
-                                for (; published < k; ++published)
-                                    mbar_arrive(&full_a[(dg + NG * published) % kWsAStages]);
-                            }
-                            if (!mbar_wait_ns(&empty_a[buf], par, kWaitNs)) *abort_v = 1;
-                        }
-                    }
-                    // a warp leaves together (the scales are exchanged between lanes)
-                    if (kTr ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
+                    // the buffer is free once the MMAs of stage s - depth completed
+                    if (s >= kWsAStages && !mbar_wait_ns(&empty_a[buf], ((s / kWsAStages) - 1) & 1, kWaitNs)) *abort_v = 1;
+                    // a warp leaves together where its lanes act together
+                    if ((kTr || Pair) ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
                         ok = false;
                         break;
                     }
                     const Chunk<S> code = code_ring[u];
                     const bool live = live_of(s);
-                    code_ring[u] = fetch(s + NG * kCodeAhead);
                     uint8_t *A = tileA + buf * kTileABytes;
                     const uint4 *books = scb + (Op::kLayers > 1 ? layer_of(s) * S::K * 256 : 0);
                     const uint4 *cb = op.w[Op::kLayers > 1 ? layer_of(s) : 0].cb;
                     if constexpr (kTr) {
-                        const uint32_t mine = scale_ring[u];
-                        scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
-                        const uint4 *cb_next = op.w[layer_of(s + NG)].cb;
-                        const Chunk<S> code_next = code_ring[(u + 1) % kCodeAhead];
+                        const uint32_t mine = float_to_half_bits(half_bits_to_float(scale_ring[u]) * inv);
                         auto put = [&](int r, uint4 v) {
                             const uint32_t h = __shfl_sync(0xffffffffu, mine, (rt_l & 1) * 8 + r);
                             const __half2 h2 = __half2half2(__ushort_as_half((uint16_t)h));
@@ -858,11 +949,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                         };
                         if constexpr (kGatherAhead) {
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                const uint4 v = ahead[r];
-                                ahead[r] = ldg_nc_v4(cb_next + code_next.code(r, 0));
-                                put(r, v);
-                            }
+                            for (int r = 0; r < 8; ++r) put(r, ahead[u & 1][r]);
                         } else if constexpr (S::K <= 2) {
                             uint4 tt[8][S::K];
 #pragma unroll
@@ -903,18 +990,18 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                         }
                     }
                 }
-                if constexpr (kAsyncWeights) {
-                    cp_async_commit();
-                    const int j = k - kLag;  // own stage whose copies have landed
-                    if (j >= published) {
-                        cp_async_wait<kLag>();
-                        fence_proxy_async_smem();
-                        mbar_arrive(&full_a[(dg + NG * j) % kWsAStages]);
-                        published = j + 1;
+                if constexpr (kAsyncWeights) cp_async_arrive(&full_a[s % kWsAStages]);
+                else publish(s);
+                // the next requests follow the fence, which would wait for them
+                code_ring[u] = fetch(s + NG * kCodeAhead);
+                if constexpr (kTr) {
+                    scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
+                    if constexpr (kGatherAhead) {
+                        const uint4 *cb_next = op.w[layer_of(s + 2 * NG)].cb;
+                        const Chunk<S> code_next = code_ring[(u + 2) % kCodeAhead];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) ahead[u & 1][r] = ldg_nc_v4(cb_next + code_next.code(r, 0));
                     }
-                } else {
-                    fence_proxy_async_smem();
-                    mbar_arrive(&full_a[s % kWsAStages]);
                 }
             }
         }
@@ -931,19 +1018,20 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         // something gave up: record it and drain what was issued (bounded)
         if (tid == 0) record_status(ws, AQ_ERR_TIMEOUT);
         if (tid == 32) mbar_wait_ns(acc_full, 0, kWaitNs);
-        if (tid == 0)
+        if (tid == 0 && half == 0)  // (pair: the leader's barriers cover both CTAs' copies)
             for (int s = max(0, nk - kWsStages); s < nk; ++s)
                 mbar_wait_ns(&full_b[s % kWsStages], (s / kWsStages) & 1, kWaitNs);
     }
     // The decoder warps finish: warp & 3 is the TMEM lane quarter, the NG
-    // warps of a quarter take alternate blocks of 16 columns.  After a
+    // warps of a quarter take alternate blocks of 64 columns (PlainOp: 16).  After a
     // timeout no tensor memory is read and the output is incomplete, which
     // the status word reports; the barriers and counters are still served.
     bool finish = warp >= 2 && *abort_v == 0;
     const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int r = (warp & 3) * 32 + lane;
     constexpr size_t kSlice = kBM * BN / 4;  // float4 per slice
-    int c = 16 * ((warp - 2) / 4), end = BN, ks = 1;
+    constexpr int kCols = Op::kStaged ? 64 : 16;
+    int c = kCols * ((warp - 2) / 4), end = BN, ks = 1;
     const float4 *slices = nullptr;
     unsigned *counter = nullptr;
     tc_fence_after();
@@ -953,7 +1041,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         float4 *mine = reinterpret_cast<float4 *>(sp.partials) + ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * ks * kSlice;
         slices = mine;
         if (finish) {
-            publish_sums<BN>(mine + (size_t)z * kSlice, tq, c, 16 * NG, z * cw, (z + 1) * cw, T - n0, r);
+            publish_sums<BN>(mine + (size_t)z * kSlice, tq, 16 * ((warp - 2) / 4), 16 * NG, z * cw, (z + 1) * cw, T - n0, r);
             fence_acq_rel_gpu();
         }
         cluster_sync_all();  // every split's sums are in L2 (every thread, also after a timeout)
@@ -964,7 +1052,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         float4 *mine = reinterpret_cast<float4 *>(reinterpret_cast<char *>(ws) + kWsData) + (size_t)tail_idx * ks * kSlice;
         slices = mine;
         counter = reinterpret_cast<unsigned *>(reinterpret_cast<char *>(ws) + kWsHeader) + tail_idx;
-        if (finish) publish_sums<BN>(mine + (size_t)z * kSlice, tq, c, 16 * NG, 0, 0, T - n0, r);
+        if (finish) publish_sums<BN>(mine + (size_t)z * kSlice, tq, 16 * ((warp - 2) / 4), 16 * NG, 0, 0, T - n0, r);
         __syncthreads();
         if (tid == 0) {
             // the barrier orders the CTA's slice stores before this increment,
@@ -976,15 +1064,25 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         __syncthreads();
         if (!*reinterpret_cast<volatile uint32_t *>(last_flag)) finish = false, counter = nullptr;
     }
-    if (finish)
-        finish_blocks(op, L, out, c, 16 * NG, end, [&](int c0, float (&v)[16]) {
-            tmem_ld16(tq + (uint32_t)c0, v);
-            if (ks > 1) add_slices<Op::kAhead>(v, slices + ((c0 / 16) * 4) * kBM + r, kSlice, ks, z);
-        });
+    if (finish) {
+        const Splits<BN> splits{slices + r, ks, z};
+        if constexpr (Op::kStaged)
+            op.dispatch([&](auto family, auto grad) {
+                finish_staged<decltype(family)::value, decltype(grad)::value, BN>(
+                    op, L, out, &maps.m[Op::kXMaps], smem, in_bar, ws, tq, c, kCols * NG, end, splits);
+            });
+        else
+            finish_direct<BN>(op, L, out, tq, c, kCols * NG, end, splits);
+    }
     if (counter && tid == 0) *counter = 0u;
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, BN);
+    if constexpr (Pair) {
+        cluster_sync_all();  // neither CTA's shared or tensor memory is in use by the other
+        if (warp == 0) tmem_dealloc_pair(tmem, BN);
+    } else {
+        if (warp == 0) tmem_dealloc(tmem, BN);
+    }
 }
 
 }  // namespace aqk
@@ -1000,12 +1098,14 @@ struct GemmPlan {
     int per_split;    // 64-deep stages per split
     bool cluster;     // the splits form one cluster and finish on chip
     TailMap tail;     // ks > 0: the tail mode's 1-D grid
+    bool pair;        // CTA pairs of two row tiles (mtiles counts pairs)
     size_t ws_bytes;  // status word + tile counters + fp32 partials
 };
 
 // `mtiles` row tiles, `nst` stages of the contraction; `max_bn` where the
-// shared memory does not hold 512-token tiles.
-inline GemmPlan plan_ws(int mtiles, int nst, int T, int max_bn = 512)
+// shared memory does not hold 512-token tiles; `pairs`: the operator may run
+// as CTA pairs (and finishes 64 columns at a time).
+inline GemmPlan plan_ws(int mtiles, int nst, int T, int max_bn = 512, bool pairs = false)
 {
     GemmPlan p{};
     p.ws_bytes = kWsHeader;
@@ -1021,10 +1121,23 @@ inline GemmPlan plan_ws(int mtiles, int nst, int T, int max_bn = 512)
     p.bn = T >= 384 || (T > 256 && (long)p.mtiles * ((T + 511) / 512) * 2 >= kNumSMs) ? 512 : 256;
     p.bn = std::min(p.bn, max_bn);
     p.ntiles = (T + p.bn - 1) / p.bn;
-    const long tiles = (long)p.mtiles * p.ntiles;
+    long tiles = (long)p.mtiles * p.ntiles, slots = kNumSMs;  // tiles and how many of them run at once
+    // 512-token tiles run as CTA pairs where a split in two at most fills
+    // the GPU (a cluster of a pair and four splits holds eight CTAs, of which
+    // only 15 fit at once)
+    if (pairs && p.bn == 512) {
+        const long t2 = (long)((mtiles + 1) / 2) * p.ntiles;
+        if (t2 * 4 > kNumSMs / 2) {
+            p.pair = true;
+            p.mtiles = (mtiles + 1) / 2;
+            tiles = t2;
+            slots = kNumSMs / 2;
+        }
+    }
+    const size_t slice = (size_t)kBM * p.bn * sizeof(float) * (p.pair ? 2 : 1);  // fp32 sums of a tile
     // the decode is the bound: split the contraction until about one CTA
     // per SM works, keeping at least 8 stages per split
-    int ks = tiles < kNumSMs ? (int)(kNumSMs / tiles) : 1;
+    int ks = tiles < slots ? (int)(slots / tiles) : 1;
     ks = std::max(1, std::min(ks, nst / 8));
     // the split runs as one thread-block cluster along z whose CTAs share
     // the finish: 2, 4 or 8 CTAs (the largest power of two not above ks).
@@ -1032,25 +1145,25 @@ inline GemmPlan plan_ws(int mtiles, int nst, int T, int max_bn = 512)
     // per = ceil(nst / kc) gives exactly kc non-empty splits
     if (ks >= 2) {
         int kc = 2;
-        while (kc * 2 <= std::min(ks, 8)) kc *= 2;
+        while (kc * 2 <= std::min(ks, p.pair ? 2 : pairs ? p.bn / 64 : 8)) kc *= 2;
         ks = kc;
     }
     p.per_split = (nst + ks - 1) / ks;
     p.ks = (nst + p.per_split - 1) / p.per_split;
     p.cluster = p.ks > 1;
-    if (p.ks > 1) p.ws_bytes = kWsData + (size_t)p.ks * tiles * kBM * p.bn * sizeof(float);
+    if (p.ks > 1) p.ws_bytes = kWsData + (size_t)p.ks * tiles * slice;
     // more tiles than one wave, the last wave at most half full: its tiles'
     // contraction is split so that it fills the SMs (Llama-2-7B MLP
     // rows at 2048 tokens: 344 tiles, 48 in the third wave, split 3 ways)
-    if (p.ks == 1 && tiles > kNumSMs) {
-        const long tail = tiles % kNumSMs;
-        if (tail > 0 && tail * 2 <= kNumSMs && tail <= kWsMaxCounters) {
-            int kt = std::min((int)(kNumSMs / tail), std::min(nst / 8, 8));
+    if (p.ks == 1 && tiles > slots) {
+        const long tail = tiles % slots;
+        if (tail > 0 && tail * 2 <= slots && tail * (p.pair ? 2 : 1) <= kWsMaxCounters) {
+            int kt = std::min((int)(slots / tail), std::min(nst / 8, 8));
             if (kt >= 2) {
                 const int per = (nst + kt - 1) / kt;
                 kt = (nst + per - 1) / per;  // no empty split
                 p.tail = TailMap{(int)(tiles - tail), kt, per};
-                p.ws_bytes = kWsData + (size_t)tail * kt * kBM * p.bn * sizeof(float);
+                p.ws_bytes = kWsData + (size_t)tail * kt * slice;
             }
         }
     }
@@ -1071,25 +1184,38 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 }
 
 // Activations [rows][T] binary16, rows `pitch` elements apart (a multiple of
-// 8): innermost dimension tokens, box 64 tokens x 64 rows.
+// 8): innermost dimension tokens, box 64 tokens x `height` rows.
 inline bool token_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map, const uint16_t *x, int rows, int T,
-                      int pitch)
+                      int pitch, int height = kBK)
 {
     cuuint64_t dims[2] = {(cuuint64_t)T, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)kBK};
+    cuuint32_t box[2] = {64, (cuuint32_t)height};
     cuuint32_t estr[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t *>(x), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class S, int BN, class Op>
+// The maps of a staged operator's arrays: the input and outputs where TMA
+// can address them (T a multiple of 8), else the outputs' padded copies.
+template <class Op>
+bool io_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, TensorMaps<Op::kMaps> *maps, const Op &op, const Geom &g, int T)
+{
+    const int pitch = (T + 7) / 8 * 8;
+    for (int i = 0; i < 5; ++i) {
+        if ((i >= 3) != (T % 8 != 0) || !op.io(i)) continue;
+        if (!token_map(encode, &maps->m[Op::kXMaps + i], op.io(i), op.rows(g), T, pitch, Op::kRows)) return false;
+    }
+    return true;
+}
+
+template <class S, int BN, class Op, bool Pair>
 constexpr int gemm_ws_smem_bytes()
 {
     constexpr int BB = kWsBookBytes<S, Op>;
-    return 1024 + kWsAStagesOf<S, BN, BB> * kTileABytes + kWsStagesOf<S, BN, BB> * (kBK * BN * 2) + BB +
-           (2 * kWsAStagesOf<S, BN, BB> + 2 * kWsStagesOf<S, BN, BB> + 1) * 8 + 16;
+    constexpr int NA = kWsAStagesOf<S, BN, BB, Pair>, NB = kWsStagesOf<S, BN, BB, Pair>;
+    return 1024 + NA * kTileABytes + NB * (kBK * BN * 2 / (Pair ? 2 : 1)) + BB + ((Pair ? 3 : 2) * NA + 2 * NB + 1 + kInBoxes<Op, BN>) * 8 + 16;
 }
 
 // 512-token tiles of two layers' 8x8 codebooks (64 KiB) do not fit.
@@ -1112,19 +1238,21 @@ cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMa
                       void *ws, cudaStream_t s, bool pdl)
 {
     const long tiles = (long)p.mtiles * p.ntiles;
-    const dim3 grid = p.tail.ks > 0 ? dim3((unsigned)(p.tail.full + (tiles - p.tail.full) * p.tail.ks), 1, 1)
-                                    : dim3(p.mtiles, p.ntiles, p.ks);
+    const unsigned width = p.pair ? 2 : 1;  // CTAs per tile
+    const dim3 grid = p.tail.ks > 0 ? dim3(width * (unsigned)(p.tail.full + (tiles - p.tail.full) * p.tail.ks), 1, 1)
+                                    : dim3(width * p.mtiles, p.ntiles, p.ks);
     GemmSplit sp{nullptr};
     if (p.ks > 1) sp.partials = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kWsData);
-    auto launch = [&](auto sch, auto bn) {
+    auto launch = [&](auto sch, auto bn, auto pair) {
         using S = decltype(sch);
         constexpr int BN = decltype(bn)::value;
+        constexpr bool Pair = decltype(pair)::value;
         if constexpr (BN > kWsMaxBN<S, Op>) {
             return cudaErrorInvalidValue;
         } else {
-            constexpr int smem = gemm_ws_smem_bytes<S, BN, Op>();
+            constexpr int smem = gemm_ws_smem_bytes<S, BN, Op, Pair>();
             static_assert(smem <= 227 * 1024, "shared memory of the warp-specialised GEMM");
-            auto kern = gemm_ws_kernel<S, BN, Op>;
+            auto kern = gemm_ws_kernel<S, BN, Op, Pair>;
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
             cudaLaunchConfig_t cfg = {};
@@ -1134,11 +1262,11 @@ cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMa
             cfg.stream = s;
             cudaLaunchAttribute attr[2];
             int na = 0;
-            if (p.cluster) {
+            if (p.cluster || Pair) {
                 attr[na].id = cudaLaunchAttributeClusterDimension;
-                attr[na].val.clusterDim.x = 1;
+                attr[na].val.clusterDim.x = width;
                 attr[na].val.clusterDim.y = 1;
-                attr[na].val.clusterDim.z = p.ks;
+                attr[na].val.clusterDim.z = p.cluster ? p.ks : 1;
                 ++na;
             }
             if (pdl) {
@@ -1154,8 +1282,10 @@ cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMa
         }
     };
     return with_scheme(g, [&](auto sch) {
-        return p.bn == 512 ? launch(sch, std::integral_constant<int, 512>{})
-                           : launch(sch, std::integral_constant<int, 256>{});
+        if constexpr (Op::kPairs)
+            if (p.pair) return launch(sch, std::integral_constant<int, 512>{}, std::true_type{});
+        return p.bn == 512 ? launch(sch, std::integral_constant<int, 512>{}, std::false_type{})
+                           : launch(sch, std::integral_constant<int, 256>{}, std::false_type{});
     });
 }
 

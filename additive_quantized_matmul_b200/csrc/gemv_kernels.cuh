@@ -100,7 +100,9 @@ __device__ __forceinline__ void store_one(const Out &out, int row, int batch, in
     v *= sc;
     if constexpr (Out::kFused) {
         if (out.ep.bias) v += half_bits_to_float(out.ep.bias[row]);
-        v = act_value(out.ep.act, v);
+        float one[1] = {v};
+        act_values(out.ep.act, one);
+        v = one[0];
         if (out.ep.residual) v += half_bits_to_float(out.ep.residual[at]);
     }
     out.y[at] = __half_as_ushort(__float2half_rn(v));

@@ -14,7 +14,7 @@ using namespace aqk;
 
 static GemmPlan plan_back(const Geom &g, int layers, int T)
 {
-    return plan_ws(ws_mtiles<BackOp>(g), layers * ws_layer_stages<BackOp>(g), T, ws_max_bn<BackOp>(g));
+    return plan_ws(ws_mtiles<BackOp>(g), layers * ws_layer_stages<BackOp>(g), T, ws_max_bn<BackOp>(g), BackOp::kPairs);
 }
 
 size_t back_plan_bytes(const Geom &g, int layers, int T) { return plan_back(g, layers, T).ws_bytes; }
@@ -24,12 +24,12 @@ cudaError_t launch_back(const Geom &g, int layers, const LayerWeights &w0, const
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
-    TensorMaps<2> maps;
+    TensorMaps<BackOp::kMaps> maps{};
+    const BackOp op{{w0, layers > 1 ? w1 : w0}, layers, gx};
     const int pitch = padded_tokens(T);
     if (!token_map(encode, &maps.m[0], g0, g.out, T, pitch) ||
-        !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch))
+        !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch) || !io_maps(encode, &maps, op, g, T))
         return cudaErrorInvalidValue;
-    const BackOp op{{w0, layers > 1 ? w1 : w0}, layers, gx};
     return launch_ws(g, plan_back(g, layers, T), maps, op, T, ws, s, true);
 }
 
