@@ -55,9 +55,29 @@ __device__ __forceinline__ float act_value(const ActParams &k, float v, float &s
         slope = fmaf(y * (1.f - p), fmaf(3.f * k.k2, v2, k.k1), p);
         return y;
     } else {
-        constexpr float kSqrtHalf = 0.7071067811865476f, kInvSqrt2Pi = 0.3989422804014327f;
-        const float cdf = 0.5f * erfcf(-v * kSqrtHalf);
-        slope = fmaf(v * kInvSqrt2Pi, __expf(-0.5f * v * v), cdf);
+        // Phi(v) = erfc(-v / sqrt(2)) / 2, erfc by the rational-argument
+        // Chebyshev fit of "Numerical Recipes" (Press et al., section
+        // "Incomplete gamma function, error function"): t exp(-x^2 + P(t)),
+        // t = 1 / (1 + x / 2), x >= 0, relative error below 1.2e-7 everywhere
+        // -- the tail of negative v keeps its bits
+        constexpr float kLog2E = 1.4426950408889634f, kInvSqrt2Pi = 0.3989422804014327f;
+        const float x = fabsf(v) * 0.7071067811865476f;
+        float t, e, g;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, x, 1.f)));
+        float q = fmaf(t, 0.17087277f, -0.82215223f);
+        q = fmaf(t, q, 1.48851587f);
+        q = fmaf(t, q, -1.13520398f);
+        q = fmaf(t, q, 0.27886807f);
+        q = fmaf(t, q, -0.18628806f);
+        q = fmaf(t, q, 0.09678418f);
+        q = fmaf(t, q, 0.37409196f);
+        q = fmaf(t, q, 1.00002368f);
+        q = fmaf(t, q, -1.26551223f);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(-kLog2E * x * x));      // exp(-v^2 / 2)
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(kLog2E * q));
+        const float tail = 0.5f * t * e * g;                                     // Phi(-|v|)
+        const float cdf = v < 0.f ? tail : 1.f - tail;
+        slope = fmaf(v * kInvSqrt2Pi, g, cdf);
         return v * cdf;
     }
 }

@@ -4,35 +4,91 @@
 // aq_glu_grad), which compute the projections again and take the gradient in
 // the epilogue, then multiply it back (input_grad.cu).
 //
-// All run on the warp-specialised kernel of gemm_ws.cuh.  TMA needs rows of
-// 16-byte multiples; for T not a multiple of 8 the activations are first
-// copied to rows of T rounded up to 8 in the workspace.
+// All run on the warp-specialised kernel of gemm_ws.cuh, whose arrays have
+// rows of 16-byte multiples (TMA).  For T not a multiple of 8 one launch
+// first copies the inputs to rows of T rounded up to 8 in the workspace, and
+// one last launch copies the results from there.  (Ragged rows read and
+// written by the kernel itself cost 15 to 40 us of epilogue at 1001 and 2047
+// tokens; the two copies cost 2 us each and the traffic.)
 #include "gemm_ws.cuh"
 #include "layer_ops.cuh"
 
 namespace aqk {
 
-// x [rows][T] -> rows of `pitch` (T rounded up to 8) elements; the elements
-// past T are left alone (the tensor maps end at T).  A thread writes one
-// 16-byte piece; a warp's reads cover 512 consecutive bytes.
-constexpr int kPadThreads = 256;
+// Rows of T elements from one pitch to another.  A warp takes 2 KiB of a row:
+// the 16-byte aligned pieces of the destination, 32 consecutive ones an
+// access, four in flight.  The source of a piece starts m bytes into an
+// aligned piece of its own, m the same for the whole row, so a lane reads one
+// aligned piece, gets the next from its neighbour and shifts; the up to seven
+// elements at either end of a row go singly.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyPieces = 128;  // pieces of a row per warp
 
-__global__ void __launch_bounds__(kPadThreads)
-pad_rows_kernel(const uint16_t *__restrict__ x, int rows, int T, int pitch, uint16_t *__restrict__ out)
+struct RowCopies {
+    aqh::RowCopy job[aqh::kMaxRowCopies];
+};
+
+// Bytes m .. m + 15 of the 32 bytes (a, b); m even, the same in every lane.
+__device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int m)
+{
+    uint32_t w[5];
+    switch (m >> 2) {
+    case 0: w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x; break;
+    case 1: w[0] = a.y, w[1] = a.z, w[2] = a.w, w[3] = b.x, w[4] = b.y; break;
+    case 2: w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z; break;
+    default: w[0] = a.w, w[1] = b.x, w[2] = b.y, w[3] = b.z, w[4] = b.w; break;
+    }
+    const int sh = 8 * (m & 2);
+    return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                      __funnelshift_r(w[3], w[4], sh));
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
 {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int per_row = pitch / 8;
-    const size_t n = (size_t)rows * per_row;
-    for (size_t i = (size_t)blockIdx.x * kPadThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kPadThreads) {
-        const size_t r = i / per_row;
-        const int c = (int)(i - r * per_row) * 8;
-        const uint16_t *src = x + r * T + c;
-        uint32_t h[8];
+    const aqh::RowCopy &c = jobs.job[blockIdx.z];
+    const int lane = threadIdx.x & 31;
+    // first byte past the source array: an aligned piece that passes it is read by elements
+    const uintptr_t src_end = reinterpret_cast<uintptr_t>(c.src + (size_t)(c.rows - 1) * c.src_pitch + T);
+    for (int r = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); r < c.rows; r += gridDim.x * (kCopyThreads / 32)) {
+        uint16_t *dst = c.dst + (size_t)r * c.dst_pitch;
+        const uint16_t *src = c.src + (size_t)r * c.src_pitch;
+        const int head = min(T, (int)((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / 2);
+        const int pieces = (T - head) / 8;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(src + head);
+        const int m = (int)(from & 15);
+        auto read = [&](int piece) {  // the aligned piece in which piece `piece`'s source starts
+            const uintptr_t at = (from & ~(uintptr_t)15) + 16 * (size_t)piece;
+            if (at + 16 <= src_end) return __ldg(reinterpret_cast<const uint4 *>(at));
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            for (int j = 0; j < 8; ++j)
+                if (at + 2 * j < src_end) w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(at + 2 * j) << (16 * (j & 1));
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        const int p0 = blockIdx.y * kCopyPieces;
+        uint4 a[kCopyPieces / 32], b[kCopyPieces / 32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = c + j < T ? (uint32_t)__ldg(src + j) : 0u;
-        *reinterpret_cast<uint4 *>(out + r * pitch + c) =
-            make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+        for (int i = 0; i < kCopyPieces / 32; ++i) {
+            const int p = p0 + 32 * i + lane;
+            if (p < pieces) a[i] = read(p);
+            // the last lane's (or piece's) neighbour is not in the warp
+            if (p < pieces && m && (lane == 31 || p == pieces - 1)) b[i] = read(p + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopyPieces / 32; ++i) {
+            const int p = p0 + 32 * i + lane;
+            uint4 n;
+            n.x = __shfl_down_sync(0xffffffffu, a[i].x, 1), n.y = __shfl_down_sync(0xffffffffu, a[i].y, 1);
+            n.z = __shfl_down_sync(0xffffffffu, a[i].z, 1), n.w = __shfl_down_sync(0xffffffffu, a[i].w, 1);
+            if (lane == 31 || p == pieces - 1) n = b[i];
+            if (p < pieces) *reinterpret_cast<uint4 *>(dst + head + 8 * (size_t)p) = bytes_from(a[i], n, m);
+        }
+        if (blockIdx.y == 0) {
+            const int tail = head + 8 * pieces;
+            if (lane < head) dst[lane] = src[lane];
+            if (lane >= 8 && tail + lane - 8 < T && lane < 16) dst[tail + lane - 8] = src[tail + lane - 8];
+        }
     }
 }
 
@@ -65,133 +121,205 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *__restrict_
 namespace aqh {
 using namespace aqk;
 
-cudaError_t pad_rows(const uint16_t *x, int rows, int T, uint16_t *out, cudaStream_t s)
+cudaError_t copy_rows(const RowCopy *jobs, int n, int T, cudaStream_t s)
 {
-    const int pitch = padded_tokens(T);
-    const size_t pieces = (size_t)rows * (pitch / 8);
-    const unsigned grid = (unsigned)std::min<size_t>((pieces + kPadThreads - 1) / kPadThreads, 16 * kNumSMs);
-    return launch_programmatic(pad_rows_kernel, dim3(grid), dim3(kPadThreads), s, x, rows, T, pitch, out);
+    RowCopies all{};
+    int rows = 0;
+    for (int i = 0; i < n; ++i) {
+        all.job[i] = jobs[i];
+        rows = std::max(rows, jobs[i].rows);
+    }
+    const unsigned pieces = (unsigned)(T / 8 + kCopyPieces) / kCopyPieces;
+    const unsigned grid = (unsigned)std::max(1, std::min((rows + 7) / 8, (int)(16 * kNumSMs / pieces) + 1));
+    return launch_programmatic(copy_rows_kernel, dim3(grid, pieces, n), dim3(kCopyThreads), s, all, T);
 }
 
 namespace {
 
-// Workspace of a product: the plan's, then (T ragged) the padded input.
+// Workspace of an operator: the plan's part (of the product, and of the
+// transposed product after it), then the sums of the bias gradient and, with T
+// ragged, the padded arrays.
 struct Layout {
     GemmPlan p;
-    size_t x_pad;   // offset of the padded input
     size_t end;
+    size_t take(size_t bytes)
+    {
+        const size_t at = align_up(end);
+        end = at + bytes;
+        return at;
+    }
 };
 
 template <class Op>
-Layout layout_of(const Geom &g, int T)
+Layout layout_of(const Geom &g, int T, bool back)
 {
     Layout l;
     l.p = plan_ws(ws_mtiles<Op>(g), ws_layer_stages<Op>(g), T, ws_max_bn<Op>(g), Op::kPairs);
-    l.x_pad = align_up(l.p.ws_bytes);
-    l.end = T % 8 ? l.x_pad + padded_bytes(g.in, T) : l.p.ws_bytes;
+    l.end = back ? std::max(l.p.ws_bytes, back_plan_bytes(g, Op::kLayers, T)) : l.p.ws_bytes;
     return l;
 }
 
-// Pads x where T asks for it and launches the product.
 template <class Op>
 cudaError_t product(const Geom &g, const Layout &l, const uint16_t *x, int T, const Op &op, char *ws, cudaStream_t s)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
-    if (T % 8) {
-        uint16_t *xp = reinterpret_cast<uint16_t *>(ws + l.x_pad);
-        const cudaError_t e = pad_rows(x, g.in, T, xp, s);
-        if (e != cudaSuccess) return e;
-        x = xp;
-    }
     TensorMaps<Op::kMaps> maps{};
-    if (!token_map(encode, &maps.m[0], x, g.in, T, padded_tokens(T)) || !io_maps(encode, &maps, op, g, T))
+    const int pitch = padded_tokens(T);
+    if (!token_map(encode, &maps.m[0], x, g.in, T, pitch) || !io_maps(encode, &maps, op, g, T, pitch))
         return cudaErrorInvalidValue;
     return launch_ws(g, l.p, maps, op, T, ws, s, true);
 }
 
-// The backward passes: the product's part (later the transposed product's
-// plan works there: it follows the product on the stream), then the sums of
-// the bias gradient and the padded copies of the gradients.
-struct GradLayout {
-    Layout l;
-    size_t sums, pad0, pad1, end;
+// An operator's arrays where the kernels see them: the caller's own, or with
+// T ragged their padded stand-ins in the workspace.
+class Arrays {
+public:
+    Arrays(Layout &l, char *ws, int T) : l_(l), ws_(ws), T_(T), pad_(T % 8 != 0) {}
+    const uint16_t *in(const uint16_t *a, int rows)
+    {
+        if (!pad_ || !a) return a;
+        uint16_t *p = room(rows);
+        in_[nin_++] = RowCopy{a, p, rows, T_, padded_tokens(T_)};
+        return p;
+    }
+    uint16_t *out(uint16_t *a, int rows)
+    {
+        if (!pad_ || !a) return a;
+        uint16_t *p = room(rows);
+        out_[nout_++] = RowCopy{p, a, rows, padded_tokens(T_), T_};
+        return p;
+    }
+    cudaError_t before(cudaStream_t s) const { return nin_ ? copy_rows(in_, nin_, T_, s) : cudaSuccess; }
+    cudaError_t after(cudaStream_t s) const { return nout_ ? copy_rows(out_, nout_, T_, s) : cudaSuccess; }
+
+private:
+    uint16_t *room(int rows) { return reinterpret_cast<uint16_t *>(ws_ + l_.take(padded_bytes(rows, T_))); }
+    Layout &l_;
+    char *ws_;
+    int T_;
+    bool pad_;
+    RowCopy in_[kMaxRowCopies], out_[kMaxRowCopies];
+    int nin_ = 0, nout_ = 0;
 };
 
-template <class Op>
-GradLayout grad_layout(const Geom &g, int T)
+// Workspace with room for padded arrays of [in] and of [out] rows.
+size_t with_padding(Layout l, const Geom &g, int T, int in_arrays, int out_arrays)
 {
-    constexpr bool kBias = !Op::kGated;
-    const size_t pad = T % 8 ? align_up(padded_bytes(g.out, T)) : 0;
-    GradLayout r;
-    r.l = layout_of<Op>(g, T);
-    r.sums = align_up(std::max(r.l.end, back_plan_bytes(g, Op::kLayers, T)));
-    r.pad0 = r.sums + (kBias ? align_up((size_t)((T + 15) / 16) * g.out * sizeof(float)) : 0);
-    r.pad1 = r.pad0 + pad;
-    r.end = r.pad1 + (Op::kLayers > 1 ? pad : 0);
-    return r;
+    if (T % 8) {
+        for (int i = 0; i < in_arrays; ++i) l.take(padded_bytes(g.in, T));
+        for (int i = 0; i < out_arrays; ++i) l.take(padded_bytes(g.out, T));
+        l.end += 128 * (size_t)(in_arrays + out_arrays);  // aligned whatever their order
+    }
+    return l.end;
 }
+
+size_t bias_sums_bytes(const Geom &g, int T) { return (size_t)((T + 15) / 16) * g.out * sizeof(float); }
 
 }  // namespace
 
-size_t gemm_fused_workspace_bytes(const Geom &g, int T) { return layout_of<FusedOp>(g, T).end; }
+size_t gemm_fused_workspace_bytes(const Geom &g, int T)
+{
+    return with_padding(layout_of<FusedOp>(g, T, false), g, T, 1, 2);
+}
 
 cudaError_t launch_gemm_fused(const Geom &g, const LayerWeights &w, const uint16_t *x, int T, const EpilogueArgs &ep,
                               uint16_t *y, void *ws, cudaStream_t s)
 {
-    const FusedOp op{{w}, ep.act, ep.bias, ep.residual, y, false, nullptr, nullptr};
-    return product(g, layout_of<FusedOp>(g, T), x, T, op, reinterpret_cast<char *>(ws), s);
+    Layout l = layout_of<FusedOp>(g, T, false);
+    char *base = reinterpret_cast<char *>(ws);
+    Arrays a(l, base, T);
+    const uint16_t *xk = a.in(x, g.in), *rk = a.in(ep.residual, g.out);
+    const FusedOp op{{w}, ep.act, ep.bias, rk, a.out(y, g.out), false, nullptr};
+    cudaError_t e = a.before(s);
+    if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
+    return e == cudaSuccess ? a.after(s) : e;
 }
 
-size_t glu_gemm_workspace_bytes(const Geom &g, int T) { return layout_of<GatedOp>(g, T).end; }
+size_t glu_gemm_workspace_bytes(const Geom &g, int T)
+{
+    return with_padding(layout_of<GatedOp>(g, T, false), g, T, 1, 1);
+}
 
 cudaError_t launch_glu_gemm(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x, int T,
                             int act, uint16_t *y, void *ws, cudaStream_t s)
 {
-    const GatedOp op{{gate, up}, act, nullptr, y, nullptr, nullptr, nullptr};
-    return product(g, layout_of<GatedOp>(g, T), x, T, op, reinterpret_cast<char *>(ws), s);
+    Layout l = layout_of<GatedOp>(g, T, false);
+    char *base = reinterpret_cast<char *>(ws);
+    Arrays a(l, base, T);
+    const uint16_t *xk = a.in(x, g.in);
+    const GatedOp op{{gate, up}, act, nullptr, a.out(y, g.out), nullptr};
+    cudaError_t e = a.before(s);
+    if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
+    return e == cudaSuccess ? a.after(s) : e;
 }
 
 size_t gemm_fused_grad_workspace_bytes(const Geom &g, int T)
 {
-    return grad_layout<FusedOp>(g, T).end;
+    Layout l = layout_of<FusedOp>(g, T, true);
+    l.take(bias_sums_bytes(g, T));
+    return with_padding(l, g, T, 2, 2);
 }
 
 cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const uint16_t *x, const uint16_t *gy, int T,
                                    const EpilogueArgs &ep, uint16_t *grad_z, float *grad_bias, uint16_t *grad_x,
                                    void *ws, cudaStream_t s)
 {
-    const GradLayout r = grad_layout<FusedOp>(g, T);
+    Layout l = layout_of<FusedOp>(g, T, true);
     char *base = reinterpret_cast<char *>(ws);
-    float *sums = grad_bias ? reinterpret_cast<float *>(base + r.sums) : nullptr;
-    uint16_t *pad = (T % 8 && grad_x) ? reinterpret_cast<uint16_t *>(base + r.pad0) : nullptr;
-    const FusedOp op{{w}, ep.act, ep.bias, gy, grad_z, true, pad, sums};
-    cudaError_t e = product(g, r.l, x, T, op, base, s);
+    float *sums = reinterpret_cast<float *>(base + l.take(bias_sums_bytes(g, T)));
+    Arrays a(l, base, T);
+    const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
+    uint16_t *zk = a.out(grad_z, g.out), *gxk = a.out(grad_x, g.in);
+    const FusedOp op{{w}, ep.act, ep.bias, gk, zk, true, grad_bias ? sums : nullptr};
+    cudaError_t e = a.before(s);
+    if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     if (e == cudaSuccess && grad_bias)
         e = launch_programmatic(bias_grad_kernel, dim3((g.out + 31) / 32), dim3(256), s, (const float *)sums,
                                 (T + 15) / 16, g.out, grad_bias);
-    if (e != cudaSuccess || !grad_x) return e;
-    return launch_back(g, 1, w, pad ? pad : grad_z, w, nullptr, T, grad_x, ws, s);
+    if (e == cudaSuccess && grad_x) e = launch_back(g, 1, w, zk, w, nullptr, T, gxk, ws, s);
+    return e == cudaSuccess ? a.after(s) : e;
 }
 
 size_t glu_grad_workspace_bytes(const Geom &g, int T)
 {
-    return grad_layout<GatedOp>(g, T).end;
+    return with_padding(layout_of<GatedOp>(g, T, true), g, T, 2, 3);
 }
 
 cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x,
                             const uint16_t *gy, int T, int act, uint16_t *grad_gate, uint16_t *grad_up,
                             uint16_t *grad_x, void *ws, cudaStream_t s)
 {
-    const GradLayout r = grad_layout<GatedOp>(g, T);
+    Layout l = layout_of<GatedOp>(g, T, true);
     char *base = reinterpret_cast<char *>(ws);
-    const bool pad = T % 8 && grad_x;
-    uint16_t *p0 = pad ? reinterpret_cast<uint16_t *>(base + r.pad0) : nullptr;
-    uint16_t *p1 = pad ? reinterpret_cast<uint16_t *>(base + r.pad1) : nullptr;
-    const GatedOp op{{gate, up}, act, gy, grad_gate, grad_up, p0, p1};
-    const cudaError_t e = product(g, r.l, x, T, op, base, s);
-    if (e != cudaSuccess || !grad_x) return e;
-    return launch_back(g, 2, gate, pad ? p0 : grad_gate, up, pad ? p1 : grad_up, T, grad_x, ws, s);
+    Arrays a(l, base, T);
+    const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
+    uint16_t *ggk = a.out(grad_gate, g.out), *guk = a.out(grad_up, g.out), *gxk = a.out(grad_x, g.in);
+    const GatedOp op{{gate, up}, act, gk, ggk, guk};
+    cudaError_t e = a.before(s);
+    if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
+    if (e == cudaSuccess && grad_x) e = launch_back(g, 2, gate, ggk, up, guk, T, gxk, ws, s);
+    return e == cudaSuccess ? a.after(s) : e;
+}
+
+size_t input_grad_workspace_bytes(const Geom &g, int T)
+{
+    Layout l;
+    l.end = back_plan_bytes(g, 1, T);
+    return with_padding(l, g, T, 1, 1);
+}
+
+cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16_t *gy, int T, uint16_t *gx, void *ws,
+                              cudaStream_t s)
+{
+    Layout l;
+    l.end = back_plan_bytes(g, 1, T);
+    Arrays a(l, reinterpret_cast<char *>(ws), T);
+    const uint16_t *gk = a.in(gy, g.out);
+    uint16_t *gxk = a.out(gx, g.in);
+    cudaError_t e = a.before(s);
+    if (e == cudaSuccess) e = launch_back(g, 1, w, gk, w, nullptr, T, gxk, ws, s);
+    return e == cudaSuccess ? a.after(s) : e;
 }
 
 }  // namespace aqh

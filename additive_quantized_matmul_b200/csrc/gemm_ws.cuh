@@ -142,9 +142,9 @@ struct TileOut {
 // turns its share into kPieces 16-byte pieces of its output row (two for 32
 // rows: all 16 tokens; one for 16 rows: tokens 8 (lane / 16) ..), reading the
 // matching pieces of its own input (residual or gradient) if it has one.
-// io() are its arrays: 0 the input, 1 and 2 the outputs, 3 and 4 second
-// copies of them with rows padded to a multiple of 8 tokens; their tensor
-// maps follow the activations' in the kernel's parameters.
+// io() are its arrays: 0 the input, 1 and 2 the outputs; their tensor maps
+// follow the activations' in the kernel's parameters (T is a multiple of 8, or
+// the rows of every array are padded to one).
 
 // y = RN16(s (W x)); T % 8 == 0.
 struct PlainOp {
@@ -160,7 +160,7 @@ struct PlainOp {
 struct FusedOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = true;
     static constexpr int kLayers = 1, kXMaps = 1, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
-    static constexpr int kMaps = kXMaps + 5;
+    static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[1];
     int act;
@@ -168,7 +168,6 @@ struct FusedOp {
     const uint16_t *in;    // residual, or gy (grad); or null
     uint16_t *out;         // y, or grad_z
     bool grad;
-    uint16_t *padded;      // grad, ragged T: a second copy of grad_z
     float *sums;           // grad: [blocks of 16 tokens][out], or null
 
     struct Row {
@@ -176,7 +175,7 @@ struct FusedOp {
     };
     __host__ __device__ const uint16_t *io(int i) const
     {
-        return i == 0 ? in : i == 1 ? out : i == 3 ? padded : nullptr;
+        return i == 0 ? in : i == 1 ? out : nullptr;
     }
     __device__ __forceinline__ int row0(const TileOut &o) const { return o.mt * kBM + (int)((threadIdx.x >> 5) & 3) * 32; }
     __host__ __device__ int rows(const Geom &L) const { return L.out; }
@@ -228,20 +227,19 @@ struct FusedOp {
 struct GatedOp {
     static constexpr bool kGated = true, kTransposed = false, kStaged = true;
     static constexpr int kLayers = 2, kXMaps = 1, kRows = 16, kPieces = 1, kOutputs = 2, kAhead = 4;
-    static constexpr int kMaps = kXMaps + 5;
+    static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[2];  // gate, up
     int act;
     const uint16_t *gy;      // or null: forward
     uint16_t *out0, *out1;   // y, -; or grad_gate, grad_up
-    uint16_t *padded0, *padded1;  // grad, ragged T: second copies
 
     struct Row {
         float sc;
     };
     __host__ __device__ const uint16_t *io(int i) const
     {
-        return i == 0 ? gy : i == 1 ? out0 : i == 2 ? out1 : i == 3 ? padded0 : padded1;
+        return i == 0 ? gy : i == 1 ? out0 : out1;
     }
     __device__ __forceinline__ int row0(const TileOut &o) const
     {
@@ -294,7 +292,7 @@ struct GatedOp {
 struct BackOp {
     static constexpr bool kGated = false, kTransposed = true, kStaged = true;
     static constexpr int kLayers = 2, kXMaps = 2, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
-    static constexpr int kMaps = kXMaps + 5;
+    static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[2];
     int layers;  // 1 or 2
@@ -386,32 +384,6 @@ struct Splits {
     }
 };
 
-// Rows row0 .. row0 + R - 1 (below nrows), tokens gn .. gn + 63 (below T), of
-// a [nrows][T] array to (load) or from a 128-byte-swizzled box: 32 lanes of
-// consecutive tokens an access.
-template <int R, bool kLoad>
-__device__ __forceinline__ void copy_rows(uint16_t *__restrict__ a, int T, int row0, int nrows, int gn, uint8_t *box)
-{
-    const int lane = threadIdx.x & 31;
-    uint16_t *p = a + (size_t)row0 * T + gn + lane;
-    const bool t0 = gn + lane < T, t1 = gn + lane + 32 < T;
-    const int live = min(R, nrows - row0);
-#pragma unroll 8
-    for (int r = 0; r < live; ++r, p += T) {
-        // token t of the row: half-word t % 8 of chunk t / 8
-        uint16_t *s0 = reinterpret_cast<uint16_t *>(box + sw128((uint32_t)r, (uint32_t)lane >> 3)) + (lane & 7);
-        uint16_t *s1 = reinterpret_cast<uint16_t *>(box + sw128((uint32_t)r, (uint32_t)(lane + 32) >> 3)) + (lane & 7);
-        if (kLoad) {
-            const uint16_t h0 = t0 ? __ldcg(p) : (uint16_t)0, h1 = t1 ? __ldcg(p + 32) : (uint16_t)0;
-            *s0 = h0;
-            *s1 = h1;
-        } else {
-            if (t0) p[0] = *s0;
-            if (t1) p[32] = *s1;
-        }
-    }
-}
-
 // A warp's share of the finish: accumulator columns [c, end) of its 32 TMEM
 // lanes at `tq`, 64 at a time, every `step`, as blocks of 16.  The next
 // block's columns are requested before a block is worked on.
@@ -458,9 +430,7 @@ __device__ __forceinline__ void finish_direct(const PlainOp &op, const Geom &L, 
 // read.  The input's boxes come by TMA, all requested at once; a lane reads
 // its pieces, writes its results over them, and the box leaves by TMA.  (One
 // row per lane straight to memory would make 32 requests of 32 bytes an
-// instruction: measured 18 to 40 thousand cycles a tile instead of 7 to 12.)
-// With T not a multiple of 8 the rows start at any even address: the warp
-// copies the box's rows itself, 64 consecutive bytes an access.
+// instruction: measured 18 to 40 thousand cycles a tile instead of 7 to 14.)
 // Not inlined: its registers are its own, and the decoders' loop keeps theirs.
 template <int Family, bool Grad, int BN, class Op>
 __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const TileOut &o, const CUtensorMap *io,
@@ -477,11 +447,10 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
     const ActParams k = act_params(op.act);
     end = min(end, o.T - o.n0);
     if (row0 >= nrows || c >= end) return;  // (a pair's second row tile may be empty)
-    const bool vec = (o.T & 7) == 0;
     const int r_lane = R == 32 ? lane : lane & 15, p_lane = R == 32 ? 0 : lane >> 4;
     auto box = [&](int cb, int a) { return stage + ((size_t)a * (BN / 64) + cb / 64) * (4 * kBox) + q * kBox; };
     const uint16_t *in = op.io(0);
-    if (in && vec && lane == 0) {
+    if (in && lane == 0) {
         fence_proxy_async_smem();
         for (int cb = c; cb < end; cb += step) {
             uint64_t *bar = &in_bar[(cb / 64) * 4 + q];
@@ -494,11 +463,7 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
         const int cb = cc & ~63, b = (cc & 63) / 16;
         uint8_t *b0 = box(cb, 0);
         if (in && b == 0) {
-            if (vec) {
-                if (!mbar_wait_ns(&in_bar[(cb / 64) * 4 + q], 0, kWaitNs)) record_status(ws, AQ_ERR_TIMEOUT);
-            } else {
-                copy_rows<R, true>(const_cast<uint16_t *>(in), o.T, row0, nrows, o.n0 + cb, b0);
-            }
+            if (!mbar_wait_ns(&in_bar[(cb / 64) * 4 + q], 0, kWaitNs)) record_status(ws, AQ_ERR_TIMEOUT);
             __syncwarp();
         }
         splits.template add<Op::kAhead>(cc, v);
@@ -518,25 +483,12 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
             if (kTwo) *reinterpret_cast<uint4 *>(b1 + at[i]) = y1[i];
         }
         if (b == 3 || cc + 16 >= end) {  // the box is complete (or the tokens are)
-            if (vec || op.io(3)) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (vec) {
-                        tma_store_2d(&io[1], smem_u32(b0), o.n0 + cb, row0);
-                        if (kTwo) tma_store_2d(&io[2], smem_u32(b1), o.n0 + cb, row0);
-                    } else {
-                        tma_store_2d(&io[3], smem_u32(b0), o.n0 + cb, row0);
-                        if (Op::kOutputs > 1 && op.io(4)) tma_store_2d(&io[4], smem_u32(b1), o.n0 + cb, row0);
-                    }
-                    bulk_commit();
-                }
-            }
-            if (!vec) {
-                __syncwarp();
-                copy_rows<R, false>(const_cast<uint16_t *>(op.io(1)), o.T, row0, nrows, o.n0 + cb, b0);
-                if (kTwo)
-                    copy_rows<R, false>(const_cast<uint16_t *>(op.io(2)), o.T, row0, nrows, o.n0 + cb, b1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&io[1], smem_u32(b0), o.n0 + cb, row0);
+                if (kTwo) tma_store_2d(&io[2], smem_u32(b1), o.n0 + cb, row0);
+                bulk_commit();
             }
         }
     });
@@ -776,10 +728,8 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             grid_dependency_wait();
             const int rows = Op::kGated ? kBM / 2 : kBM;
             for (int i = lane; i < rows && mt * rows + i < L.out; i += 32) {
-                const uintptr_t p = reinterpret_cast<uintptr_t>(in + (size_t)(mt * rows + i) * T + n0);
-                const uintptr_t e = p + 2 * (size_t)min(BN, T - n0), a = p & ~(uintptr_t)15;
-                if (((e - a) & ~(uintptr_t)15) > 0)
-                    prefetch_l2_bulk(reinterpret_cast<const void *>(a), (uint32_t)((e - a) & ~(uintptr_t)15));
+                const int pitch = (T + 7) & ~7;
+                prefetch_l2_bulk(in + (size_t)(mt * rows + i) * pitch + n0, 2u * (uint32_t)min(BN, pitch - n0));
             }
             __syncwarp();
         }
@@ -1144,8 +1094,12 @@ inline GemmPlan plan_ws(int mtiles, int nst, int T, int max_bn = 512, bool pairs
     // With at least 8 stages per split (nst >= 8 kc) none of them is empty:
     // per = ceil(nst / kc) gives exactly kc non-empty splits
     if (ks >= 2) {
+        // (staged operators own whole blocks of 64 columns per split, and take
+        // 8 splits only where all their clusters run at once: 15 of 8 full-SM
+        // CTAs fit; 18 clusters measured 2x the time of a split in 4)
+        const int most = p.pair ? 2 : !pairs ? 8 : (p.bn < 512 || tiles > 15) ? 4 : 8;
         int kc = 2;
-        while (kc * 2 <= std::min(ks, p.pair ? 2 : pairs ? p.bn / 64 : 8)) kc *= 2;
+        while (kc * 2 <= std::min(ks, most)) kc *= 2;
         ks = kc;
     }
     p.per_split = (nst + ks - 1) / ks;
@@ -1197,16 +1151,14 @@ inline bool token_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *map
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The maps of a staged operator's arrays: the input and outputs where TMA
-// can address them (T a multiple of 8), else the outputs' padded copies.
+// The maps of a staged operator's arrays, rows `pitch` elements apart.
 template <class Op>
-bool io_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, TensorMaps<Op::kMaps> *maps, const Op &op, const Geom &g, int T)
+bool io_maps(PFN_cuTensorMapEncodeTiled_v12000 encode, TensorMaps<Op::kMaps> *maps, const Op &op, const Geom &g, int T,
+             int pitch)
 {
-    const int pitch = (T + 7) / 8 * 8;
-    for (int i = 0; i < 5; ++i) {
-        if ((i >= 3) != (T % 8 != 0) || !op.io(i)) continue;
-        if (!token_map(encode, &maps->m[Op::kXMaps + i], op.io(i), op.rows(g), T, pitch, Op::kRows)) return false;
-    }
+    for (int i = 0; i < 3; ++i)
+        if (op.io(i) && !token_map(encode, &maps->m[Op::kXMaps + i], op.io(i), op.rows(g), T, pitch, Op::kRows))
+            return false;
     return true;
 }
 

@@ -255,8 +255,8 @@ __device__ __forceinline__ void prefetch_range_scales(const Geom &L, const Out &
 // meanwhile.
 // Without it (or with fewer than 16 ks bytes) they are summed straight
 // from L2, eight slots in flight per float4.
-template <int kInFlight = 8, class Out>
-__device__ __forceinline__ void splitk_finish(const Geom &L, SplitK sk, int counter, int ks, int row0,
+template <int kInFlight, class Out>
+__device__ __forceinline__ void splitk_finish_body(const Geom &L, SplitK sk, int counter, int ks, int row0,
                                               int nrows, int batch, const Out &out, float4 *stage, int stage_bytes)
 {
     constexpr bool kTwo = Out::kGated || Out::kFused;  // a second row parameter: up's scale, or the bias
@@ -362,6 +362,26 @@ __device__ __forceinline__ void splitk_finish(const Geom &L, SplitK sk, int coun
         __syncthreads();  // the next pass reuses the staging area
     }
     if (threadIdx.x == 0) sk.counters[counter] = 0u;
+}
+
+// The fused forms' finish is a function of its own: inlined, its activation
+// code costs the main loops registers (the gated table kernel 19.2 us against
+// 16.3 at 11008 x 4096).
+template <int kInFlight, class Out>
+__device__ __noinline__ void splitk_finish_outlined(const Geom &L, SplitK sk, int counter, int ks, int row0, int nrows,
+                                                    int batch, const Out &out, float4 *stage, int stage_bytes)
+{
+    splitk_finish_body<kInFlight>(L, sk, counter, ks, row0, nrows, batch, out, stage, stage_bytes);
+}
+
+template <int kInFlight = 8, class Out>
+__device__ __forceinline__ void splitk_finish(const Geom &L, SplitK sk, int counter, int ks, int row0, int nrows,
+                                              int batch, const Out &out, float4 *stage, int stage_bytes)
+{
+    if constexpr (Out::kFused || Out::kGated)
+        splitk_finish_outlined<kInFlight>(L, sk, counter, ks, row0, nrows, batch, out, stage, stage_bytes);
+    else
+        splitk_finish_body<kInFlight>(L, sk, counter, ks, row0, nrows, batch, out, stage, stage_bytes);
 }
 
 // ---------------------------------------------------------------------------
@@ -615,7 +635,15 @@ gemv_lut_kernel(Geom L, const __grid_constant__ Out out, const uint16_t *__restr
                             h[j * K + k] = *reinterpret_cast<const __half *>(
                                 lutb + lut_offset<S>(ch[j], r, k, lane4) + q * 128 + half * 2);
                         }
-                    acc[r] = __half2float(__hadd(__hadd(h[0], h[1]), __hadd(h[2], h[3])));
+                    // aq_gemv adds the four in binary16; the fused forms, whose
+                    // results pass through an activation, in fp32 (error of a
+                    // gated 11008 x 4096 layer 6.7e-4 -> 5.0e-4 of the result;
+                    // 3.5e-4 of it is the tables' leaving out the rounding of
+                    // each decoded weight, which finer entries do not mend)
+                    if constexpr (Out::kFused || Out::kGated)
+                        acc[r] = (__half2float(h[0]) + __half2float(h[1])) + (__half2float(h[2]) + __half2float(h[3]));
+                    else
+                        acc[r] = __half2float(__hadd(__hadd(h[0], h[1]), __hadd(h[2], h[3])));
                 } else {
                     float a = 0.f;
 #pragma unroll

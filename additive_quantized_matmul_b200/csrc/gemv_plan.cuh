@@ -127,12 +127,20 @@ inline bool plan_rf(const Geom &g, int batch, size_t cap, int layers, GemvPlan &
         if (ws_of(gc4) > cap || (ks * layers > 1 && nrb > kWsMaxCounters)) continue;
         const long ctas = (long)nrb * ks * layers;
         const long per_sm = (ctas + kNumSMs - 1) / kNumSMs;  // CTAs on the busiest SM
-        const double load = (double)per_sm * gc4 + (per_sm > per_sm_slots ? 1e9 : 0);  // groups it works through
+        double load = (double)per_sm * gc4 + (per_sm > per_sm_slots ? 1e9 : 0);  // groups it works through
+        // a gated block has twice the CTAs, often more than fit at once: then
+        // the waves count, each with a fixed cost of about 24 groups (1x16
+        // 11008 x 4096 at batch 16: 5 splits in 3 waves of 104 groups, 62 us;
+        // 2 splits in 2 waves of 256, 73 us; 8 splits 72 us)
+        if (layers > 1) {
+            const long slots = (long)per_sm_slots * kNumSMs;
+            load = ctas <= slots ? (double)per_sm * (gc4 + 24) / per_sm_slots : (double)((ctas + slots - 1) / slots) * (gc4 + 24);
+        }
         if (best == 0 || load < best) {
             best = load;
             gc = gc4;
         }
-        if (ctas > (long)per_sm_slots * kNumSMs) break;
+        if (ctas > (long)per_sm_slots * kNumSMs * (layers > 1 ? 8 : 1)) break;
     }
     const int ks = (g.G + gc - 1) / gc;
     if (ws_of(gc) > cap || (ks * layers > 1 && nrb > kWsMaxCounters)) return false;
@@ -146,7 +154,9 @@ inline bool plan_rf(const Geom &g, int batch, size_t cap, int layers, GemvPlan &
     // row block stages all its splits' partial sums in one pass (one L2
     // round trip), while the CTAs an SM holds still fit
     const size_t stage = (size_t)ks * layers * rows * batch * sizeof(float) + (k2 ? RfTraits<Scheme<2, 8>>::kBookBytes : 0);
-    const int cap_smem = (per_sm_slots == 1 ? 220 : 113) * 1024;
+    // (a gated 1x16 block keeps more of L1 for its two codebooks instead: 62
+    // against 66 us at batch 16)
+    const int cap_smem = (per_sm_slots == 1 ? 220 : layers > 1 ? 40 : 113) * 1024;
     p.cc_smem = std::max(smem(gc), (int)std::min<size_t>(stage, (size_t)cap_smem));
     return true;
 }

@@ -28,27 +28,9 @@ cudaError_t launch_back(const Geom &g, int layers, const LayerWeights &w0, const
     const BackOp op{{w0, layers > 1 ? w1 : w0}, layers, gx};
     const int pitch = padded_tokens(T);
     if (!token_map(encode, &maps.m[0], g0, g.out, T, pitch) ||
-        !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch) || !io_maps(encode, &maps, op, g, T))
+        !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch) || !io_maps(encode, &maps, op, g, T, pitch))
         return cudaErrorInvalidValue;
     return launch_ws(g, plan_back(g, layers, T), maps, op, T, ws, s, true);
-}
-
-size_t input_grad_workspace_bytes(const Geom &g, int T)
-{
-    const size_t plan = back_plan_bytes(g, 1, T);
-    return T % 8 ? align_up(plan) + padded_bytes(g.out, T) : plan;
-}
-
-cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16_t *gy, int T, uint16_t *gx, void *ws,
-                              cudaStream_t s)
-{
-    if (T % 8) {
-        uint16_t *pad = reinterpret_cast<uint16_t *>(reinterpret_cast<char *>(ws) + align_up(back_plan_bytes(g, 1, T)));
-        const cudaError_t e = pad_rows(gy, g.out, T, pad, s);
-        if (e != cudaSuccess) return e;
-        gy = pad;
-    }
-    return launch_back(g, 1, w, gy, w, nullptr, T, gx, ws, s);
 }
 
 }  // namespace aqh

@@ -10,11 +10,20 @@ inline int padded_tokens(int T) { return (T + 7) / 8 * 8; }
 inline size_t align_up(size_t v) { return (v + 127) / 128 * 128; }
 inline size_t padded_bytes(int rows, int T) { return (size_t)rows * padded_tokens(T) * sizeof(uint16_t); }
 
-// x [rows][T] into rows of padded_tokens(T) elements.
-cudaError_t pad_rows(const uint16_t *x, int rows, int T, uint16_t *out, cudaStream_t s);
+// Rows of T elements from one pitch to another (the padding is left alone).
+struct RowCopy {
+    const uint16_t *src;
+    uint16_t *dst;
+    int rows, src_pitch, dst_pitch;
+};
+constexpr int kMaxRowCopies = 3;
+
+// Up to three arrays in one launch.
+cudaError_t copy_rows(const RowCopy *jobs, int n, int T, cudaStream_t s);
 
 // The transposed product over one or two layers, g0 and g1 [out] rows of
-// padded_tokens(T) elements; its plan works in the first back_plan_bytes of ws.
+// padded_tokens(T) elements, gx likewise; its plan works in the first
+// back_plan_bytes of ws.
 size_t back_plan_bytes(const aqk::Geom &g, int layers, int T);
 cudaError_t launch_back(const aqk::Geom &g, int layers, const aqk::LayerWeights &w0, const uint16_t *g0,
                         const aqk::LayerWeights &w1, const uint16_t *g1, int T, uint16_t *gx, void *ws,
