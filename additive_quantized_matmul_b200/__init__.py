@@ -161,10 +161,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """Address of torch's current stream (without building a Stream object
+    where torch offers that: 0.5 us of a call against 3)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

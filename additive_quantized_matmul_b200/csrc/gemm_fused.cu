@@ -20,12 +20,16 @@ namespace aqk {
 // access, four in flight.  The source of a piece starts m bytes into an
 // aligned piece of its own, m the same for the whole row, so a lane reads one
 // aligned piece, gets the next from its neighbour and shifts; the up to seven
-// elements at either end of a row go singly.
+// elements at either end of a row go singly.  With scales (a whole launch's
+// arrays are multiplied, by 2^-E alone where an array has none) each element
+// is rounded once.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPieces = 128;  // pieces of a row per warp
 
 struct RowCopies {
     aqh::RowCopy job[aqh::kMaxRowCopies];
+    int jobs;
+    float *factor;  // with scales: receives 2^E
 };
 
 // Bytes m .. m + 15 of the 32 bytes (a, b); m even, the same in every lane.
@@ -49,11 +53,28 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
     grid_launch_dependents();
     const aqh::RowCopy &c = jobs.job[blockIdx.z];
     const int lane = threadIdx.x & 31;
+    float inv = 1.f;
+    if (jobs.factor) {  // some job has scales: every CTA finds the largest
+        __shared__ uint32_t s_max;
+        if (threadIdx.x == 0) s_max = 0;
+        __syncthreads();
+        uint32_t m = 0;
+        for (int j = 0; j < jobs.jobs; ++j)
+            m = max(m, jobs.job[j].scales ? absmax_share(jobs.job[j].scales, jobs.job[j].rows, threadIdx.x, kCopyThreads)
+                                          : 0x3c00u);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) atomicMax(&s_max, m);
+        __syncthreads();
+        const int e = scale_exponent(s_max);
+        inv = ldexpf(1.f, -e);
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *jobs.factor = ldexpf(1.f, e);
+    }
     // first byte past the source array: an aligned piece that passes it is read by elements
     const uintptr_t src_end = reinterpret_cast<uintptr_t>(c.src + (size_t)(c.rows - 1) * c.src_pitch + T);
     for (int r = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); r < c.rows; r += gridDim.x * (kCopyThreads / 32)) {
         uint16_t *dst = c.dst + (size_t)r * c.dst_pitch;
         const uint16_t *src = c.src + (size_t)r * c.src_pitch;
+        const float sc = c.scales ? half_bits_to_float(__ldg(c.scales + r)) * inv : inv;
         const int head = min(T, (int)((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15) / 2);
         const int pieces = (T - head) / 8;
         const uintptr_t from = reinterpret_cast<uintptr_t>(src + head);
@@ -82,12 +103,17 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
             n.x = __shfl_down_sync(0xffffffffu, a[i].x, 1), n.y = __shfl_down_sync(0xffffffffu, a[i].y, 1);
             n.z = __shfl_down_sync(0xffffffffu, a[i].z, 1), n.w = __shfl_down_sync(0xffffffffu, a[i].w, 1);
             if (lane == 31 || p == pieces - 1) n = b[i];
-            if (p < pieces) *reinterpret_cast<uint4 *>(dst + head + 8 * (size_t)p) = bytes_from(a[i], n, m);
+            if (p < pieces) {
+                uint4 v = bytes_from(a[i], n, m);
+                if (jobs.factor) v = scale_round_h8(v, sc);
+                *reinterpret_cast<uint4 *>(dst + head + 8 * (size_t)p) = v;
+            }
         }
         if (blockIdx.y == 0) {
             const int tail = head + 8 * pieces;
-            if (lane < head) dst[lane] = src[lane];
-            if (lane >= 8 && tail + lane - 8 < T && lane < 16) dst[tail + lane - 8] = src[tail + lane - 8];
+            const int e = lane < 8 ? lane : tail + lane - 8;
+            if (lane < 8 ? lane < head : lane < 16 && e < T)
+                dst[e] = jobs.factor ? float_to_half_bits(sc * half_bits_to_float(src[e])) : src[e];
         }
     }
 }
@@ -121,16 +147,21 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *__restrict_
 namespace aqh {
 using namespace aqk;
 
-cudaError_t copy_rows(const RowCopy *jobs, int n, int T, cudaStream_t s)
+cudaError_t copy_rows(const RowCopy *jobs, int n, int T, float *factor, cudaStream_t s)
 {
     RowCopies all{};
+    all.jobs = n;
+    for (int i = 0; i < n; ++i)
+        if (jobs[i].scales) all.factor = factor;
     int rows = 0;
     for (int i = 0; i < n; ++i) {
         all.job[i] = jobs[i];
         rows = std::max(rows, jobs[i].rows);
     }
-    const unsigned pieces = (unsigned)(T / 8 + kCopyPieces) / kCopyPieces;
-    const unsigned grid = (unsigned)std::max(1, std::min((rows + 7) / 8, (int)(16 * kNumSMs / pieces) + 1));
+    const unsigned pieces = (unsigned)std::max(1, (T / 8 + kCopyPieces - 1) / kCopyPieces);
+    // (with scales every CTA reads all of them, so there are fewer: four per SM)
+    const int ctas = (all.factor ? 4 : 16) * kNumSMs / (int)(pieces * (all.factor ? n : 1)) + 1;
+    const unsigned grid = (unsigned)std::max(1, std::min((rows + 7) / 8, ctas));
     return launch_programmatic(copy_rows_kernel, dim3(grid, pieces, n), dim3(kCopyThreads), s, all, T);
 }
 
@@ -180,18 +211,18 @@ public:
     {
         if (!pad_ || !a) return a;
         uint16_t *p = room(rows);
-        in_[nin_++] = RowCopy{a, p, rows, T_, padded_tokens(T_)};
+        in_[nin_++] = RowCopy{a, p, rows, T_, padded_tokens(T_), nullptr};
         return p;
     }
     uint16_t *out(uint16_t *a, int rows)
     {
         if (!pad_ || !a) return a;
         uint16_t *p = room(rows);
-        out_[nout_++] = RowCopy{p, a, rows, padded_tokens(T_), T_};
+        out_[nout_++] = RowCopy{p, a, rows, padded_tokens(T_), T_, nullptr};
         return p;
     }
-    cudaError_t before(cudaStream_t s) const { return nin_ ? copy_rows(in_, nin_, T_, s) : cudaSuccess; }
-    cudaError_t after(cudaStream_t s) const { return nout_ ? copy_rows(out_, nout_, T_, s) : cudaSuccess; }
+    cudaError_t before(cudaStream_t s) const { return nin_ ? copy_rows(in_, nin_, T_, nullptr, s) : cudaSuccess; }
+    cudaError_t after(cudaStream_t s) const { return nout_ ? copy_rows(out_, nout_, T_, nullptr, s) : cudaSuccess; }
 
 private:
     uint16_t *room(int rows) { return reinterpret_cast<uint16_t *>(ws_ + l_.take(padded_bytes(rows, T_))); }
@@ -212,6 +243,36 @@ size_t with_padding(Layout l, const Geom &g, int T, int in_arrays, int out_array
         l.end += 128 * (size_t)(in_arrays + out_arrays);  // aligned whatever their order
     }
     return l.end;
+}
+
+// The gradients that the transposed product reads: as they are, or (1x16
+// layers with scales) copies multiplied by the scales, in one launch.
+struct Scaled {
+    const uint16_t *g[2];
+    const float *factor;  // or null
+};
+
+size_t scaled_bytes(const Geom &g, int T, int layers)
+{
+    return back_takes_scaled(g) ? layers * (align_up(padded_bytes(g.out, T)) + 128) + 256 : 0;
+}
+
+// `pitch`: of the gradients in memory (T where they are ragged and unpadded).
+cudaError_t scale_gradients(const Geom &g, Layout &l, char *ws, int layers, const LayerWeights *w,
+                            const uint16_t *const *grads, int T, int pitch, Scaled *out, cudaStream_t s)
+{
+    *out = Scaled{{grads[0], layers > 1 ? grads[1] : grads[0]}, nullptr};
+    const bool scales = w[0].scales || (layers > 1 && w[1].scales);
+    if (!back_takes_scaled(g) || (!scales && pitch == padded_tokens(T))) return cudaSuccess;
+    float *factor = reinterpret_cast<float *>(ws + l.take(sizeof(float)));
+    RowCopy jobs[2];
+    for (int i = 0; i < layers; ++i) {
+        uint16_t *z = reinterpret_cast<uint16_t *>(ws + l.take(padded_bytes(g.out, T)));
+        jobs[i] = RowCopy{grads[i], z, g.out, pitch, padded_tokens(T), w[i].scales};
+        out->g[i] = z;
+    }
+    if (scales) out->factor = factor;
+    return copy_rows(jobs, layers, T, factor, s);
 }
 
 size_t bias_sums_bytes(const Geom &g, int T) { return (size_t)((T + 15) / 16) * g.out * sizeof(float); }
@@ -258,7 +319,7 @@ size_t gemm_fused_grad_workspace_bytes(const Geom &g, int T)
 {
     Layout l = layout_of<FusedOp>(g, T, true);
     l.take(bias_sums_bytes(g, T));
-    return with_padding(l, g, T, 2, 2);
+    return with_padding(l, g, T, 2, 2) + scaled_bytes(g, T, 1);
 }
 
 cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const uint16_t *x, const uint16_t *gy, int T,
@@ -277,13 +338,17 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
     if (e == cudaSuccess && grad_bias)
         e = launch_programmatic(bias_grad_kernel, dim3((g.out + 31) / 32), dim3(256), s, (const float *)sums,
                                 (T + 15) / 16, g.out, grad_bias);
-    if (e == cudaSuccess && grad_x) e = launch_back(g, 1, w, zk, w, nullptr, T, gxk, ws, s);
+    if (e == cudaSuccess && grad_x) {
+        Scaled z;
+        e = scale_gradients(g, l, base, 1, &w, &zk, T, padded_tokens(T), &z, s);
+        if (e == cudaSuccess) e = launch_back(g, 1, w, z.g[0], w, nullptr, T, z.factor, gxk, ws, s);
+    }
     return e == cudaSuccess ? a.after(s) : e;
 }
 
 size_t glu_grad_workspace_bytes(const Geom &g, int T)
 {
-    return with_padding(layout_of<GatedOp>(g, T, true), g, T, 2, 3);
+    return with_padding(layout_of<GatedOp>(g, T, true), g, T, 2, 3) + scaled_bytes(g, T, 2);
 }
 
 cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x,
@@ -298,7 +363,13 @@ cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const Layer
     const GatedOp op{{gate, up}, act, gk, ggk, guk};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
-    if (e == cudaSuccess && grad_x) e = launch_back(g, 2, gate, ggk, up, guk, T, gxk, ws, s);
+    if (e == cudaSuccess && grad_x) {
+        const LayerWeights w[2] = {gate, up};
+        const uint16_t *grads[2] = {ggk, guk};
+        Scaled z;
+        e = scale_gradients(g, l, base, 2, w, grads, T, padded_tokens(T), &z, s);
+        if (e == cudaSuccess) e = launch_back(g, 2, gate, z.g[0], up, z.g[1], T, z.factor, gxk, ws, s);
+    }
     return e == cudaSuccess ? a.after(s) : e;
 }
 
@@ -306,7 +377,7 @@ size_t input_grad_workspace_bytes(const Geom &g, int T)
 {
     Layout l;
     l.end = back_plan_bytes(g, 1, T);
-    return with_padding(l, g, T, 1, 1);
+    return with_padding(l, g, T, 1, 1) + scaled_bytes(g, T, 1);
 }
 
 cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16_t *gy, int T, uint16_t *gx, void *ws,
@@ -314,11 +385,15 @@ cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16
 {
     Layout l;
     l.end = back_plan_bytes(g, 1, T);
-    Arrays a(l, reinterpret_cast<char *>(ws), T);
-    const uint16_t *gk = a.in(gy, g.out);
+    char *base = reinterpret_cast<char *>(ws);
+    Arrays a(l, base, T);
+    const bool scaled = back_takes_scaled(g);  // one launch pads and scales
+    const uint16_t *gk = scaled ? gy : a.in(gy, g.out);
     uint16_t *gxk = a.out(gx, g.in);
     cudaError_t e = a.before(s);
-    if (e == cudaSuccess) e = launch_back(g, 1, w, gk, w, nullptr, T, gxk, ws, s);
+    Scaled z;
+    if (e == cudaSuccess) e = scale_gradients(g, l, base, 1, &w, &gk, T, scaled ? T : padded_tokens(T), &z, s);
+    if (e == cudaSuccess) e = launch_back(g, 1, w, z.g[0], w, nullptr, T, z.factor, gxk, ws, s);
     return e == cudaSuccess ? a.after(s) : e;
 }
 

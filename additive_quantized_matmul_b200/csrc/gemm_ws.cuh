@@ -38,10 +38,9 @@
 //    runs over the layer's rows (of one or two layers, one after the other):
 //    thread t decodes chunk (row tile t/16, group t%16) and its codewords
 //    lie along M, so A is MN-major like B.  The row scale belongs to the
-//    contraction index and is multiplied into the weights (one rounding to
-//    binary16 each, after division by the power of two 2^E just above the
-//    largest scale, so that nothing overflows and uniformly small scales
-//    lose no bits; 2^E is applied to the fp32 sums).
+//    contraction index and is multiplied, divided by 2^E (scale_exponent),
+//    into the weights or, before, into the other operand: one rounding to
+//    binary16 each; 2^E is applied to the fp32 sums.
 #pragma once
 
 #include <cuda.h>
@@ -149,6 +148,7 @@ struct TileOut {
 // y = RN16(s (W x)); T % 8 == 0.
 struct PlainOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = false;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kMaps = 1, kXMaps = 1, kAhead = 4;
     static constexpr bool kPairs = false;
     LayerWeights w[1];
@@ -159,6 +159,7 @@ struct PlainOp {
 // act'(z)) and the sums of gy act'(z) over each block of 16 tokens.
 struct FusedOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = true;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kXMaps = 1, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -226,6 +227,7 @@ struct FusedOp {
 // Gated block: y = RN16(act(g) u), or, with gy, the gradients of g and u.
 struct GatedOp {
     static constexpr bool kGated = true, kTransposed = false, kStaged = true;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 2, kXMaps = 1, kRows = 16, kPieces = 1, kOutputs = 2, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -288,15 +290,21 @@ struct GatedOp {
     }
 };
 
-// gx = RN16(sum over the layers of W^T (s gy)).
+// gx = RN16(sum over the layers of W^T (s gy)).  Scaled: gy comes multiplied
+// by s / 2^E, and the weights go into shared memory as they are (1x16: by
+// asynchronous copies; scaling them on the way through registers took 2207
+// cycles a stage against 1400); else the decoders scale the weights.
+template <bool Scaled>
 struct BackOp {
     static constexpr bool kGated = false, kTransposed = true, kStaged = true;
+    static constexpr bool kScaleWeights = !Scaled;
     static constexpr int kLayers = 2, kXMaps = 2, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[2];
     int layers;  // 1 or 2
     uint16_t *gx;
+    const float *factor;  // Scaled: 2^E
     static constexpr int act = AQ_ACT_NONE;
 
     struct Row {
@@ -537,27 +545,6 @@ __device__ __forceinline__ void publish_sums(float4 *slice, uint32_t tq, int c, 
 
 // ---- kernel -------------------------------------------------------------------
 
-// Largest |v| (as the bits of a binary16; NaN above infinity) of this
-// thread's share of v[0 .. n), `threads` threads in all.
-__device__ __forceinline__ uint32_t absmax_share(const uint16_t *__restrict__ v, int n, int thread, int threads)
-{
-    uint32_t m = 0;
-    // 16-byte pieces between the ragged ends (v has 2-byte alignment)
-    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(v) & 15)) & 15) / 2);
-    const int nv = (n - head) / 8;
-    const uint4 *v4 = reinterpret_cast<const uint4 *>(v + head);
-#pragma unroll 8
-    for (int i = thread; i < nv; i += threads) {
-        const uint4 q = __ldg(v4 + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
-    }
-    if (thread < head) m = max(m, (uint32_t)v[thread] & 0x7fffu);
-    if (head + nv * 8 + thread < n && thread < 8) m = max(m, (uint32_t)v[head + nv * 8 + thread] & 0x7fffu);
-    return m;
-}
-
 // Barrier of the decoder threads alone (the CTA's other warps do not take part).
 __device__ __forceinline__ void decoder_barrier(int threads)
 {
@@ -575,7 +562,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     constexpr int kWsTileB = kBK * BN * 2 / (Pair ? 2 : 1);    // 32 or 64 KiB
     constexpr int kN = BN < 256 ? BN : 256;  // N of one MMA instruction
     constexpr int NG = kWsGroupsOf<S>;       // decoder groups
-    constexpr bool kTr = Op::kTransposed;
+    constexpr bool kTr = Op::kTransposed, kScaleW = Op::kScaleWeights;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -591,7 +578,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     uint64_t *in_bar = acc_full + 1;            // kStaged: the input's boxes, one per 64 tokens and lane quarter
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_bar + kInBoxes<Op, BN>);
     uint32_t *abort_flag = tmem_slot + 1;
-    uint32_t *scale_max = abort_flag + 1;       // kTransposed: largest |s| (binary16 bits)
+    uint32_t *scale_max = abort_flag + 1;       // kScaleW: largest |s| (binary16 bits)
     uint32_t *last_flag = scale_max + 1;        // the last split of a tail tile
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -626,9 +613,9 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     const int nk = max(0, min(all_stages, s0 + per) - s0);
 
     // 1x16: codewords go from L2 into the tile by cp.async, copies of kWsLag
-    // stages in flight; other schemes, and the transposed product (whose
-    // weights are scaled on the way), decode in registers
-    constexpr bool kAsyncWeights = (S::K == 1 && S::B == 16) && !kTr;
+    // stages in flight; other schemes, and weights that are scaled on the way,
+    // decode in registers
+    constexpr bool kAsyncWeights = (S::K == 1 && S::B == 16) && !kScaleW;
     if (S::B == 16 && tid == 0) prefetch_table_share(op.w[0].cb, (uint32_t)S::K * 65536u * 16u);
     if constexpr (S::B == 16 && Op::kLayers > 1)
         if (tid == 32) prefetch_table_share(op.w[1].cb, (uint32_t)S::K * 65536u * 16u);
@@ -822,7 +809,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         Chunk<S> code_ring[kCodeAhead];
 #pragma unroll
         for (int q = 0; q < kCodeAhead; ++q) code_ring[q] = fetch(dg + NG * q);
-        // kTransposed: the rows' scales, one per lane (rows of the warp's two
+        // kScaleW: the rows' scales, one per lane (rows of the warp's two
         // row tiles), as far ahead as the codes; divided by 2^E where used
         float inv = 1.f;
         uint16_t scale_ring[kCodeAhead];
@@ -832,18 +819,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             const uint16_t *sc = op.w[l].scales;
             return sc ? __ldg(sc + o) : (uint16_t)0x3c00;
         };
-        // kTransposed, one 16-bit codebook: the codewords of the next two own
-        // stages (4096 reads in flight per SM)
-        constexpr bool kGatherAhead = kTr && S::K == 1 && S::B == 16;
-        uint4 ahead[2][8];
-        if constexpr (kTr) {
-            if constexpr (kGatherAhead) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        ahead[q][r] = ldg_nc_v4(op.w[layer_of(dg + NG * q)].cb + code_ring[q].code(r, 0));
-            }
+        if constexpr (kScaleW) {
             grid_dependency_wait();  // the scales
 #pragma unroll
             for (int q = 0; q < kCodeAhead; ++q) scale_ring[q] = fetch_scale(dg + NG * q);
@@ -854,11 +830,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             if (lane == 0) atomicMax(scale_max, m);
             decoder_barrier(128 * NG);
             m = *reinterpret_cast<volatile uint32_t *>(scale_max);
-            // 2^E just above the largest |s| (1 if all are zero; 2^16 covers
-            // every finite value, infinities and NaN go through)
-            int e = 0;
-            if (m >= 0x7c00u) e = 16;
-            else if (m) e = ilogbf(half_bits_to_float((uint16_t)m)) + 1;
+            const int e = scale_exponent(m);
             inv = ldexpf(1.f, -e);
             out.factor = ldexpf(1.f, e);
         }
@@ -874,7 +846,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     // the buffer is free once the MMAs of stage s - depth completed
                     if (s >= kWsAStages && !mbar_wait_ns(&empty_a[buf], ((s / kWsAStages) - 1) & 1, kWaitNs)) *abort_v = 1;
                     // a warp leaves together where its lanes act together
-                    if ((kTr || Pair) ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
+                    if ((kScaleW || Pair) ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
                         ok = false;
                         break;
                     }
@@ -883,7 +855,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     uint8_t *A = tileA + buf * kTileABytes;
                     const uint4 *books = scb + (Op::kLayers > 1 ? layer_of(s) * S::K * 256 : 0);
                     const uint4 *cb = op.w[Op::kLayers > 1 ? layer_of(s) : 0].cb;
-                    if constexpr (kTr) {
+                    if constexpr (kScaleW) {
                         const uint32_t mine = float_to_half_bits(half_bits_to_float(scale_ring[u]) * inv);
                         auto put = [&](int r, uint4 v) {
                             const uint32_t h = __shfl_sync(0xffffffffu, mine, (rt_l & 1) * 8 + r);
@@ -897,10 +869,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                             }
                             *reinterpret_cast<uint4 *>(A + slot_of(r)) = make_uint4(p[0], p[1], p[2], p[3]);
                         };
-                        if constexpr (kGatherAhead) {
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) put(r, ahead[u & 1][r]);
-                        } else if constexpr (S::K <= 2) {
+                        if constexpr (S::K <= 2) {
                             uint4 tt[8][S::K];
 #pragma unroll
                             for (int r = 0; r < 8; ++r) gather_terms<S>(code, r, books, cb, tt[r]);
@@ -917,9 +886,12 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     } else if constexpr (kAsyncWeights) {
                         const uint32_t a0 = smem_u32(A);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            cp_async16(a0 + slot_of(r), live ? (const void *)(cb + code.code(r, 0)) : (const void *)cb,
-                                       live ? 16u : 0u);
+                        for (int r = 0; r < 8; ++r) {
+                            // kTr: a row past the layer is zero, whatever its padding code selects
+                            const bool in = live && (!kTr || tile_of(s) * 8 + r < L.out);
+                            cp_async16(a0 + slot_of(r), in ? (const void *)(cb + code.code(r, 0)) : (const void *)cb,
+                                       in ? 16u : 0u);
+                        }
                     } else if constexpr (S::K <= 2) {
                         // all codeword reads before the first tile store (the
                         // books and the tile share one shared array)
@@ -944,15 +916,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                 else publish(s);
                 // the next requests follow the fence, which would wait for them
                 code_ring[u] = fetch(s + NG * kCodeAhead);
-                if constexpr (kTr) {
-                    scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
-                    if constexpr (kGatherAhead) {
-                        const uint4 *cb_next = op.w[layer_of(s + 2 * NG)].cb;
-                        const Chunk<S> code_next = code_ring[(u + 2) % kCodeAhead];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) ahead[u & 1][r] = ldg_nc_v4(cb_next + code_next.code(r, 0));
-                    }
-                }
+                if constexpr (kScaleW) scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
             }
         }
         cp_async_wait<0>();
@@ -972,6 +936,8 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             for (int s = max(0, nk - kWsStages); s < nk; ++s)
                 mbar_wait_ns(&full_b[s % kWsStages], (s / kWsStages) & 1, kWaitNs);
     }
+    if constexpr (kTr && !kScaleW)
+        if (op.factor) out.factor = __ldcg(op.factor);
     // The decoder warps finish: warp & 3 is the TMEM lane quarter, the NG
     // warps of a quarter take alternate blocks of 64 columns (PlainOp: 16).  After a
     // timeout no tensor memory is read and the output is incomplete, which
@@ -1185,8 +1151,8 @@ int ws_max_bn(const Geom &g)
     return bn;
 }
 
-template <class Op>
-cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMaps> &maps, const Op &op, int T,
+template <class S, class Op>
+cudaError_t launch_ws_scheme(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMaps> &maps, const Op &op, int T,
                       void *ws, cudaStream_t s, bool pdl)
 {
     const long tiles = (long)p.mtiles * p.ntiles;
@@ -1195,8 +1161,7 @@ cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMa
                                     : dim3(width * p.mtiles, p.ntiles, p.ks);
     GemmSplit sp{nullptr};
     if (p.ks > 1) sp.partials = reinterpret_cast<float *>(reinterpret_cast<char *>(ws) + kWsData);
-    auto launch = [&](auto sch, auto bn, auto pair) {
-        using S = decltype(sch);
+    auto launch = [&](auto bn, auto pair) {
         constexpr int BN = decltype(bn)::value;
         constexpr bool Pair = decltype(pair)::value;
         if constexpr (BN > kWsMaxBN<S, Op>) {
@@ -1233,12 +1198,17 @@ cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMa
             return cudaGetLastError();
         }
     };
-    return with_scheme(g, [&](auto sch) {
-        if constexpr (Op::kPairs)
-            if (p.pair) return launch(sch, std::integral_constant<int, 512>{}, std::true_type{});
-        return p.bn == 512 ? launch(sch, std::integral_constant<int, 512>{}, std::false_type{})
-                           : launch(sch, std::integral_constant<int, 256>{}, std::false_type{});
-    });
+    if constexpr (Op::kPairs)
+        if (p.pair) return launch(std::integral_constant<int, 512>{}, std::true_type{});
+    return p.bn == 512 ? launch(std::integral_constant<int, 512>{}, std::false_type{})
+                       : launch(std::integral_constant<int, 256>{}, std::false_type{});
+}
+
+template <class Op>
+cudaError_t launch_ws(const Geom &g, const GemmPlan &p, const TensorMaps<Op::kMaps> &maps, const Op &op, int T,
+                      void *ws, cudaStream_t s, bool pdl)
+{
+    return with_scheme(g, [&](auto sch) { return launch_ws_scheme<decltype(sch)>(g, p, maps, op, T, ws, s, pdl); });
 }
 
 }  // namespace aqh

@@ -12,7 +12,9 @@ using namespace aqk;
 cudaError_t launch_gemv_fused(const Geom &g, const LayerWeights &w, const uint16_t *x, int batch,
                               const EpilogueArgs &ep, uint16_t *y, void *ws, cudaStream_t s)
 {
-    return launch_plan(g, plan_gemv(g, batch), GemvFusedOut{{w}, y, ep}, x, batch, ws, s, true);
+    const GemvPlan p = plan_gemv(g, batch);
+    if (ep.act == AQ_ACT_NONE) return launch_plan(g, p, GemvFusedOut<false>{{w}, y, ep}, x, batch, ws, s, true);
+    return launch_plan(g, p, GemvFusedOut<true>{{w}, y, ep}, x, batch, ws, s, true);
 }
 
 static GemvPlan plan_glu(const Geom &g, int batch) { return plan_gemv(g, batch, ~(size_t)0, 2); }

@@ -44,25 +44,28 @@ struct SplitK {
 
 // What becomes of a product's sums, and whose weights a CTA reads.
 //  * GemvOut: y = RN16(s sum), one layer (aq_gemv).
-//  * GemvFusedOut: y = RN16(act(s sum + bias) + residual).
+//  * GemvFusedOut: y = RN16(act(s sum + bias) + residual); Act false: no
+//    activation, the common case of a projection back to the residual stream,
+//    whose finish is short enough to stay inline.
 //  * GemvGatedOut: two layers, y = RN16(act(s_g sum_g) s_u sum_u).  blockIdx.z
 //    is the layer: a CTA works on one of them (its codebooks, tables or
 //    replicas are that layer's alone), writes its sums to the layer's slots
 //    even when the sum is not split, and the last CTA of a row range, of both
 //    layers' splits, joins them.
 struct GemvOut {
-    static constexpr bool kGated = false, kFused = false;
+    static constexpr bool kGated = false, kFused = false, kAct = false;
     LayerWeights w[1];
     uint16_t *y;
 };
+template <bool Act>
 struct GemvFusedOut {
-    static constexpr bool kGated = false, kFused = true;
+    static constexpr bool kGated = false, kFused = true, kAct = Act;
     LayerWeights w[1];
     uint16_t *y;
     EpilogueArgs ep;
 };
 struct GemvGatedOut {
-    static constexpr bool kGated = true, kFused = false;
+    static constexpr bool kGated = true, kFused = false, kAct = true;
     LayerWeights w[2];  // gate, up
     uint16_t *y;
     int act;
@@ -100,9 +103,11 @@ __device__ __forceinline__ void store_one(const Out &out, int row, int batch, in
     v *= sc;
     if constexpr (Out::kFused) {
         if (out.ep.bias) v += half_bits_to_float(out.ep.bias[row]);
-        float one[1] = {v};
-        act_values(out.ep.act, one);
-        v = one[0];
+        if constexpr (Out::kAct) {
+            float one[1] = {v};
+            act_values(out.ep.act, one);
+            v = one[0];
+        }
         if (out.ep.residual) v += half_bits_to_float(out.ep.residual[at]);
     }
     out.y[at] = __half_as_ushort(__float2half_rn(v));
@@ -204,7 +209,7 @@ __device__ __forceinline__ void finish_fused4(const Geom &L, const Out &out, int
         const float b = rows.s1 ? rows.s1[r] : (out.ep.bias ? half_bits_to_float(out.ep.bias[row]) : 0.f);
         v[c] = fmaf(sc, v[c], b);
     }
-    act_values(out.ep.act, v);
+    if constexpr (Out::kAct) act_values(out.ep.act, v);
     if (out.ep.residual) v[0] += r0.x, v[1] += r0.y, v[2] += r1.x, v[3] += r1.y;
     finish_write4(L, out.y, row0, idx, batch, v);
 }
@@ -364,9 +369,9 @@ __device__ __forceinline__ void splitk_finish_body(const Geom &L, SplitK sk, int
     if (threadIdx.x == 0) sk.counters[counter] = 0u;
 }
 
-// The fused forms' finish is a function of its own: inlined, its activation
-// code costs the main loops registers (the gated table kernel 19.2 us against
-// 16.3 at 11008 x 4096).
+// A finish with an activation is a function of its own: inlined, its code
+// costs the main loops registers (the gated table kernel 19.2 us against 16.3
+// at 11008 x 4096).
 template <int kInFlight, class Out>
 __device__ __noinline__ void splitk_finish_outlined(const Geom &L, SplitK sk, int counter, int ks, int row0, int nrows,
                                                     int batch, const Out &out, float4 *stage, int stage_bytes)
@@ -378,7 +383,7 @@ template <int kInFlight = 8, class Out>
 __device__ __forceinline__ void splitk_finish(const Geom &L, SplitK sk, int counter, int ks, int row0, int nrows,
                                               int batch, const Out &out, float4 *stage, int stage_bytes)
 {
-    if constexpr (Out::kFused || Out::kGated)
+    if constexpr (Out::kAct)
         splitk_finish_outlined<kInFlight>(L, sk, counter, ks, row0, nrows, batch, out, stage, stage_bytes);
     else
         splitk_finish_body<kInFlight>(L, sk, counter, ks, row0, nrows, batch, out, stage, stage_bytes);

@@ -397,12 +397,13 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  * Input gradient of a layer, the transposed product: for L = sum(gy * y) with
  * y = diag(s) W x,
  *   gx[i][t] = RN16(sum_o W[o][i] s[o] gy[o][t]),   gy [out][T], gx [in][T],
- * 1 <= T <= 2^22.  The tensor cores multiply gy by RN16(s[o] 2^-E W[o][i]),
- * where 2^E is the power of two just above the largest |s| (so that no
- * weight overflows and small scales lose no bits), and 2^E is applied to the
- * fp32 sum: each weight carries one rounding of at most 2^-11 of its value
- * plus 2^(E-25).  gx overlaps no input.  Together with aq_param_grad this is
- * the backward pass of aq_gemm.  Deterministic; the workspace holds
+ * 1 <= T <= 2^22.  The tensor cores take binary16 operands, so s is multiplied
+ * into one of them, divided by 2^E, the power of two just above the largest
+ * |s| (nothing overflows, and uniformly small scales lose no bits): into the
+ * weights, or for 1x16 layers into gy.  That operand carries one rounding of at
+ * most 2^-11 of its value plus 2^-25; 2^E is applied to the fp32 sum.  gx
+ * overlaps no input.  Together with aq_param_grad this is the backward pass of
+ * aq_gemm.  Deterministic; the workspace holds
  * aq_input_grad_workspace_bytes(desc, T) bytes.
  */
 size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T);

@@ -73,9 +73,12 @@ class Ref:
             sg = r.s[:, None] * gv
             A = np.abs(r.W).T @ np.abs(sg)
             total = total + r.W.T @ sg
-            # a scale may be subnormal once divided by 2^E (2^-25 of it), the product too
+            # a scale may be subnormal once divided by 2^E (2^-25 of it); so may
+            # its product with the weight or (1x16) with the gradient
+            small = np.abs(r.W).T @ np.ones_like(gv) if r.spec.nbits == 16 and r.spec.num_codebooks == 1 \
+                else np.abs(gv).sum(0)[None, :]
             err = err + (1.01 * H + (terms + 64) * F) * A \
-                + SUB * two_e * ((1 + np.abs(r.W).T) @ np.abs(gv))
+                + SUB * two_e * (small + np.abs(r.W).T @ np.abs(gv))
             if r.spec.num_codebooks == 8:
                 err = err + 2 * H * A
         return total, err + rounded(total)
