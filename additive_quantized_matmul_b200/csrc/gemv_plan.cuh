@@ -336,7 +336,12 @@ cudaError_t launch_plan(const Geom &g, const GemvPlan &p, const Out &out, const 
         else
             e = batch <= 8 ? rf(Scheme<1, 16>{}, One{}) : rf(Scheme<1, 16>{}, Two{});
     } else if (p.path == kLut) {
-        const int smem = kLutSmem;  // the tables and the code rings
+        // The tables and the code rings.  The fused forms ask for enough to have
+        // an SM to themselves: with room for a second CTA, launches in a row can
+        // settle into a state where some SMs hold two CTAs of one launch and
+        // others none (eager calls back to back, 11008 x 4096 at one token:
+        // gated 13.2 or 20 us, with SiLU 8.6 or 12.3; alone 13.3 and 8.9)
+        const int smem = Out::kFused || Out::kGated ? std::max(kLutSmem, 112 * 1024) : kLutSmem;
         auto lut = [&](auto sch) {
             using S = decltype(sch);
             if constexpr (S::B == 8 && S::K <= 2) {
