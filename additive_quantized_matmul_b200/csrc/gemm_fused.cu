@@ -142,6 +142,29 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const float *__restrict_
     }
 }
 
+// Without an activation: grad_z = gy, grad_bias its row sums (lane l adds the
+// tokens l, l + 32, ..., then the lanes in a tree).  One warp per row.
+__global__ void __launch_bounds__(256) linear_grad_kernel(const uint16_t *__restrict__ gy, int out, int T,
+                                                          uint16_t *__restrict__ grad_z, float *__restrict__ grad_bias)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int o = blockIdx.x * 8 + (threadIdx.x >> 5); o < out; o += gridDim.x * 8) {
+        const size_t row = (size_t)o * T;
+        float a = 0.f;
+#pragma unroll 8
+        for (int t = lane; t < T; t += 32) {
+            const uint16_t h = __ldg(gy + row + t);
+            grad_z[row + t] = h;
+            a += half_bits_to_float(h);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+        if (lane == 0 && grad_bias) grad_bias[o] = a;
+    }
+}
+
 }  // namespace aqk
 
 namespace aqh {
@@ -326,6 +349,11 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
                                    const EpilogueArgs &ep, uint16_t *grad_z, float *grad_bias, uint16_t *grad_x,
                                    void *ws, cudaStream_t s)
 {
+    if (ep.act == AQ_ACT_NONE) {  // z is not needed
+        const cudaError_t e = launch_programmatic(linear_grad_kernel, dim3(std::min((g.out + 7) / 8, 8 * kNumSMs)),
+                                                  dim3(256), s, gy, g.out, T, grad_z, grad_bias);
+        return e == cudaSuccess && grad_x ? launch_input_grad(g, w, gy, T, grad_x, ws, s) : e;
+    }
     Layout l = layout_of<FusedOp>(g, T, true);
     char *base = reinterpret_cast<char *>(ws);
     float *sums = reinterpret_cast<float *>(base + l.take(bias_sums_bytes(g, T)));

@@ -18,13 +18,24 @@
 //   warps 2-5  (and 6-9) decoders, then epilogue: thread t of a group owns
 //              one code chunk (8 rows x one group) of each of its stages.
 //              1x16: the 8 codewords go from the L2-resident codebook
-//              straight into the swizzled A tile by 16-byte cp.async, a few
-//              stages ahead; 2x8: codewords come from the codebooks in
-//              shared memory, summed with binary16 adds.  Each thread fences
-//              its writes to the async proxy and arrives on full_a[stage]
-//              (128 arrivals).  The epilogue reads TMEM lanes 32*(warp%4)..
-//              with tcgen05.ld and hands each row's sums, 16 tokens at a
-//              time, to the operator.
+//              straight into the swizzled A tile by 16-byte cp.async, as
+//              many stages ahead as the ring is deep; 2x8: codewords come
+//              from the codebooks in shared memory, summed with binary16
+//              adds, and each thread fences its writes to the async proxy.
+//              128 arrivals on full_a[stage].  The epilogue reads TMEM lanes
+//              32*(warp%4).. with tcgen05.ld and hands each row's sums, 16
+//              tokens at a time, to the operator.
+//
+// Pairs (512-token tiles of every operator but the plain product): two CTAs
+// with a row tile each run as one for tcgen05 (cta_group::2, M 256).  Each
+// holds its own W tile and half of X, so X comes from L2 and is written to
+// shared memory once for both; the even CTA issues the MMAs, on barriers that
+// both arrive on.  What bounds the main loop is the SM's shared memory (128
+// bytes a clock): per stage the MMAs read 64 KiB of operands (96 KiB
+// unpaired), TMA writes 32 (64), and the decode takes 1024 single 16-byte
+// fills (1x16) or about 800 wavefronts of random codeword reads and tile
+// writes (2x8).  Measured cycles a stage at 1.7 GHz, unpaired and paired:
+// 1x16 2157 -> 1399, 2x8 1500 -> 1255; the MMAs alone take 1024.
 //
 // The operator (Op) says what the tile's rows are, where the weights come
 // from and what becomes of the sums:
@@ -86,7 +97,6 @@ template <class S>
 constexpr int kWsGroupsOf = (S::K <= 2) ? 2 : 1;
 template <class S>
 constexpr int kWsThreadsOf = 64 + 128 * kWsGroupsOf<S>;  // X producer, MMA issuer, decoders
-constexpr int kWsLag = 2;                     // cp.async stages in flight per decoder (< ring depth)
 
 // Layers whose 8-bit codebooks a CTA keeps in shared memory.
 template <class S, class Op>
@@ -612,9 +622,10 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     const int s0 = z * per;
     const int nk = max(0, min(all_stages, s0 + per) - s0);
 
-    // 1x16: codewords go from L2 into the tile by cp.async, copies of kWsLag
-    // stages in flight; other schemes, and weights that are scaled on the way,
-    // decode in registers
+    // 1x16: codewords go from L2 into the tile by cp.async, as many stages in
+    // flight as the ring holds (the copies arrive on the stage's barrier
+    // themselves, and the MMA issuer orders them before its reads); other
+    // schemes, and weights that are scaled on the way, decode in registers
     constexpr bool kAsyncWeights = (S::K == 1 && S::B == 16) && !kScaleW;
     if (S::B == 16 && tid == 0) prefetch_table_share(op.w[0].cb, (uint32_t)S::K * 65536u * 16u);
     if constexpr (S::B == 16 && Op::kLayers > 1)
@@ -939,9 +950,9 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     if constexpr (kTr && !kScaleW)
         if (op.factor) out.factor = __ldcg(op.factor);
     // The decoder warps finish: warp & 3 is the TMEM lane quarter, the NG
-    // warps of a quarter take alternate blocks of 64 columns (PlainOp: 16).  After a
-    // timeout no tensor memory is read and the output is incomplete, which
-    // the status word reports; the barriers and counters are still served.
+    // warps of a quarter take alternate blocks of 64 columns (PlainOp: 16).
+    // After a timeout no tensor memory is read and the output is incomplete,
+    // which the status word reports; the barriers and counters are still served.
     bool finish = warp >= 2 && *abort_v == 0;
     const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int r = (warp & 3) * 32 + lane;
