@@ -107,8 +107,8 @@ int aq_version(void);
 size_t aq_packed_codes_bytes(const aq_layer_desc *desc);
 
 /*
- * Workspace.  aq_gemv, aq_gemm, aq_param_grad and aq_encode take a
- * caller-owned device workspace.  Its first 16 bytes hold a status word that
+ * Workspace.  aq_gemv, aq_gemm, aq_param_grad, aq_encode and the layer
+ * operators further down take a caller-owned device workspace.  Its first 16 bytes hold a status word that
  * a kernel sets when a bounded wait gives up (read it with
  * aq_workspace_status); then come split-K arrival counters in a fixed area
  * of 4 KiB, then the call's own data (split-K partial sums, tables).  A
@@ -384,6 +384,11 @@ typedef struct {
  * previous work on the stream.  AQ_ERR_INVALID_ARG for an unknown
  * activation or y = x; AQ_ERR_MISALIGNED for a residual off a 16-byte or a
  * bias off a 2-byte boundary.
+ * With one or two 8-bit codebooks at batch 1 the products come from lookup
+ * tables, as in aq_gemv (the layer's sums of codewords enter unrounded, each
+ * table entry rounded to binary16); the looked-up entries are added in fp32.
+ * For T not a multiple of 8 aq_gemm_fused makes three launches (rows that TMA
+ * can address are built in the workspace and copied back), else one.
  */
 size_t aq_gemm_fused_workspace_bytes(const aq_layer_desc *desc, int T);
 aq_status aq_gemv_fused(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
