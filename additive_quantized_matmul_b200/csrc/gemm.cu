@@ -1,4 +1,6 @@
-// Prefill product Y = diag(s) W X on the 5th-generation tensor cores (sm_100a).
+// Prefill product Y = diag(s) W X on the 5th-generation tensor cores (sm_100a):
+// the launcher of aq_gemm, which runs on the warp-specialised kernel of
+// gemm_ws.cuh (PlainOp) for T a multiple of 8, and the kernel for the others.
 //
 // W is decoded tile by tile from its codes (AQLM wiki entry, "Niveau
 // intermédiaire": each group of 8 weights is sum_k C_k[i_k]) straight into
@@ -7,7 +9,8 @@
 // thread issues tcgen05.mma (kind::f16: binary16 operands, fp32 accumulator
 // in tensor memory).  Tile: M = 128 rows of W, N = 128 tokens, K = 64 input
 // features (8 code groups) per stage, two stages so that decoding stage
-// k+1 overlaps the MMAs of stage k.  The epilogue reads the accumulator with
+// k+1 overlaps the MMAs of stage k; X rows are read with plain loads, which
+// TMA could not address.  The epilogue reads the accumulator with
 // tcgen05.ld, applies the row scale and rounds to binary16.
 //
 // Every wait is bounded (wall-clock limit via %globaltimer): on give-up the

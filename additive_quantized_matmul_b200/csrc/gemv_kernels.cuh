@@ -8,7 +8,7 @@
 // 8) and multiplied with the matching 8 activations, the product the
 // paper's abstract names for token generation.
 //
-// Three kernels, chosen by scheme, batch and shape:
+// Four kernels, chosen by scheme, batch and shape:
 //  * 8-bit codes with one or two codebooks (1x8, 2x8), batch 1 --
 //    `gemv_lut_kernel`: per-group codebook x activation tables in shared
 //    memory, lane-private so random codes never conflict; K 4-byte table
@@ -17,6 +17,8 @@
 //    SMs without more than 32 splits per row range) -- `gemv_1x16_cc_kernel`:
 //    codewords read into registers through L1 and multiplied with x on the
 //    CUDA cores, no tile in shared memory.
+//  * 1x16 at larger batches and 2x8 from batch 2 -- `gemv_rf_kernel`: weights
+//    decoded into mma.sync register fragments, no decoded tile in memory.
 //  * every other case -- `gemv_tc_kernel`: codes are decoded into a 128x64
 //    binary16 tile in shared memory (128-byte-swizzled, K-major) and
 //    multiplied by the activations on the tensor cores (tcgen05.mma,
