@@ -13,10 +13,10 @@
 //
 // The products are bound by the SM's shared memory and, when calls follow one
 // another, by the power limit (see gemm_ws.cuh).  In series, 2048 tokens:
-// 4096 x 11008 1x16 with residual 190 us (971 TFLOP/s, 70 % of the tensor
-// rate measured over seconds), gated 2 x 11008 x 4096 2x8 341 us (1084, 78 %),
-// backward of the gated block, 1x16, 823 us (897 counting the products computed
-// again, 65 %).  Alone: 160, 298 and 713 us.
+// 4096 x 11008 1x16 with residual 183 to 193 us (955 TFLOP/s, 69 % of the tensor
+// rate measured over seconds), gated 2 x 11008 x 4096 2x8 333 to 345 us (1069,
+// 77 %), backward of the gated block, 1x16, 790 to 829 us (891 counting the
+// products computed again, 64 %).  Alone: 160, 298 and 748 us.
 #include "gemm_ws.cuh"
 #include "layer_ops.cuh"
 
@@ -29,9 +29,9 @@ namespace aqk {
 // aligned piece, gets the next from its neighbour and shifts; the up to seven
 // elements at either end of a row go singly.  With scales (a whole launch's
 // arrays are multiplied, by 2^-E alone where an array has none) each element
-// is rounded once.  Bound by HBM and, where the arrays fit it, L2: two scaled
-// arrays of 11008 rows and 2048 tokens (90 MB read, 90 MB written) 42 us with
-// cold caches.
+// is rounded once.  Bound by the latency of its round trips: two scaled arrays of
+// 11008 rows and 2048 tokens (90 MB read, 90 MB written) 42 us with cold caches,
+// which is why aligned ones have scale_rows_kernel.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPieces = 128;  // pieces of a row per warp
 
@@ -56,6 +56,22 @@ __device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int m)
                       __funnelshift_r(w[3], w[4], sh));
 }
 
+// Every CTA looks through all the scales.
+__device__ __forceinline__ int largest_scale_exponent(const RowCopies &jobs)
+{
+    __shared__ uint32_t s_max;
+    if (threadIdx.x == 0) s_max = 0;
+    __syncthreads();
+    uint32_t m = 0;
+    for (int j = 0; j < jobs.jobs; ++j)
+        m = max(m, jobs.job[j].scales ? absmax_share(jobs.job[j].scales, jobs.job[j].rows, threadIdx.x, kCopyThreads)
+                                      : 0x3c00u);
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_max, m);
+    __syncthreads();
+    return scale_exponent(s_max);
+}
+
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
 {
     grid_dependency_wait();
@@ -63,18 +79,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
     const aqh::RowCopy &c = jobs.job[blockIdx.z];
     const int lane = threadIdx.x & 31;
     float inv = 1.f;
-    if (jobs.factor) {  // some job has scales: every CTA finds the largest
-        __shared__ uint32_t s_max;
-        if (threadIdx.x == 0) s_max = 0;
-        __syncthreads();
-        uint32_t m = 0;
-        for (int j = 0; j < jobs.jobs; ++j)
-            m = max(m, jobs.job[j].scales ? absmax_share(jobs.job[j].scales, jobs.job[j].rows, threadIdx.x, kCopyThreads)
-                                          : 0x3c00u);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) atomicMax(&s_max, m);
-        __syncthreads();
-        const int e = scale_exponent(s_max);
+    if (jobs.factor) {  // some job has scales
+        const int e = largest_scale_exponent(jobs);
         inv = ldexpf(1.f, -e);
         if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *jobs.factor = ldexpf(1.f, e);
     }
@@ -123,6 +129,46 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
             const int e = lane < 8 ? lane : tail + lane - 8;
             if (lane < 8 ? lane < head : lane < 16 && e < T)
                 dst[e] = jobs.factor ? float_to_half_bits(sc * half_bits_to_float(src[e])) : src[e];
+        }
+    }
+}
+
+// The same for scaled rows of T = pitch, a multiple of 8: every piece is aligned
+// in both arrays.  A warp takes 2 KiB of a row, the next row's share requested
+// before this one's is multiplied, the first before the scales are looked
+// through; 48 registers leave room for five CTAs an SM (64 and four above).
+// Beside copy_rows_kernel, whole calls: backward of a gated block, 1x16, 2 x
+// 11008 rows, 2048 tokens 765 -> 747 us alone (793 -> 791 in series, where power
+// bounds it); input gradients of 11008 rows, 1024 tokens 111.5 -> 109.2, of 4096
+// rows, 512 tokens 36.1 -> 35.2.
+__global__ void __launch_bounds__(kCopyThreads, 5) scale_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
+{
+    constexpr int kN = kCopyPieces / 32;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const aqh::RowCopy &c = jobs.job[blockIdx.z];
+    const int lane = threadIdx.x & 31, pieces = T / 8, step = gridDim.x * (kCopyThreads / 32);
+    const int p0 = blockIdx.y * kCopyPieces + lane;
+    auto read = [&](int r, uint4 (&a)[kN]) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(c.src + (size_t)r * T);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (p0 + 32 * i < pieces) a[i] = __ldg(src + p0 + 32 * i);
+    };
+    int r = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+    uint4 a[kN] = {}, b[kN] = {};
+    if (r < c.rows) read(r, a);
+    const int e = largest_scale_exponent(jobs);
+    const float inv = ldexpf(1.f, -e);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *jobs.factor = ldexpf(1.f, e);
+    for (; r < c.rows; r += step) {
+        if (r + step < c.rows) read(r + step, b);
+        const float sc = c.scales ? half_bits_to_float(__ldg(c.scales + r)) * inv : inv;
+        uint4 *dst = reinterpret_cast<uint4 *>(c.dst + (size_t)r * T);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            if (p0 + 32 * i < pieces) dst[p0 + 32 * i] = scale_round_h8(a[i], sc);
+            a[i] = b[i];
         }
     }
 }
@@ -209,10 +255,14 @@ cudaError_t copy_rows(const RowCopy *jobs, int n, int T, float *factor, cudaStre
         rows = std::max(rows, jobs[i].rows);
     }
     const unsigned pieces = (unsigned)std::max(1, (T / 8 + kCopyPieces - 1) / kCopyPieces);
-    // (with scales every CTA reads all of them, so there are fewer: four per SM)
-    const int ctas = (all.factor ? 4 : 16) * kNumSMs / (int)(pieces * (all.factor ? n : 1)) + 1;
-    const unsigned grid = (unsigned)std::max(1, std::min((rows + 7) / 8, ctas));
-    return launch_programmatic(copy_rows_kernel, dim3(grid, pieces, n), dim3(kCopyThreads), s, all, T);
+    const int share = (int)pieces * (all.factor ? n : 1);
+    auto grid = [&](int per_sm) {
+        return dim3(std::max(1, std::min((rows + 7) / 8, per_sm * kNumSMs / share + 1)), pieces, n);
+    };
+    // with scales every CTA reads all of them: one wave
+    if (all.factor && T % 8 == 0)
+        return launch_programmatic(scale_rows_kernel, grid(5), dim3(kCopyThreads), s, all, T);
+    return launch_programmatic(copy_rows_kernel, grid(all.factor ? 4 : 16), dim3(kCopyThreads), s, all, T);
 }
 
 namespace {

@@ -5,8 +5,8 @@
 // A CTA takes 128 input features and 256 or 512 tokens and walks the layer's
 // rows, 64 a stage: the codewords of 8 rows x 16 groups are laid along M
 // (MN-major A), gy rows come by TMA.  Two layers follow one another in the
-// same accumulator.  4096 x 4096 1x16, 512 tokens: 36 us in series, of which
-// the scaling of gy takes 6, the main loop 14 (32 tiles, the layer's rows split
+// same accumulator.  4096 x 4096 1x16, 512 tokens: 35 us in series, of which
+// the scaling of gy takes 5, the main loop 14 (32 tiles, the layer's rows split
 // over clusters of four) and the joined finish 11; 11008 x 4096 2x8, 2047
 // tokens: 206 us (896 TFLOP/s), 171 alone.
 #include "gemm_ws.cuh"
