@@ -268,17 +268,22 @@ cudaError_t copy_rows(const RowCopy *jobs, int n, int T, float *factor, cudaStre
 namespace {
 
 // Workspace of an operator: the plan's part (of the product, and of the
-// transposed product after it), then the sums of the bias gradient and, with T
-// ragged, the padded arrays.
+// transposed product after it), then the sums of the bias gradient, with T
+// ragged the padded arrays, and the scaled gradients.  An unsplit plan ends
+// before the arrival counters, which are other calls' as well as its own: an
+// array never starts among them.  A call takes some of the arrays that the
+// sizes below take, in another order: the spare bytes of `size` cover the
+// alignment.
 struct Layout {
     GemmPlan p;
     size_t end;
     size_t take(size_t bytes)
     {
-        const size_t at = align_up(end);
+        const size_t at = align_up(std::max(end, kWsData));
         end = at + bytes;
         return at;
     }
+    size_t size() const { return end > kWsData ? end + 128 : end; }
 };
 
 template <class Op>
@@ -334,15 +339,12 @@ private:
     int nin_ = 0, nout_ = 0;
 };
 
-// Workspace with room for padded arrays of [in] and of [out] rows.
-size_t with_padding(Layout l, const Geom &g, int T, int in_arrays, int out_arrays)
+// Room for padded arrays of [in] and of [out] rows.
+void take_padded(Layout &l, const Geom &g, int T, int in_arrays, int out_arrays)
 {
-    if (T % 8) {
-        for (int i = 0; i < in_arrays; ++i) l.take(padded_bytes(g.in, T));
-        for (int i = 0; i < out_arrays; ++i) l.take(padded_bytes(g.out, T));
-        l.end += 128 * (size_t)(in_arrays + out_arrays);  // aligned whatever their order
-    }
-    return l.end;
+    if (T % 8 == 0) return;
+    for (int i = 0; i < in_arrays; ++i) l.take(padded_bytes(g.in, T));
+    for (int i = 0; i < out_arrays; ++i) l.take(padded_bytes(g.out, T));
 }
 
 // The gradients that the transposed product reads: as they are, or (1x16
@@ -352,9 +354,11 @@ struct Scaled {
     const float *factor;  // or null
 };
 
-size_t scaled_bytes(const Geom &g, int T, int layers)
+void take_scaled(Layout &l, const Geom &g, int T, int layers)
 {
-    return back_takes_scaled(g) ? layers * (align_up(padded_bytes(g.out, T)) + 128) + 256 : 0;
+    if (!back_takes_scaled(g)) return;
+    l.take(sizeof(float));
+    for (int i = 0; i < layers; ++i) l.take(padded_bytes(g.out, T));
 }
 
 // `pitch`: of the gradients in memory (T where they are ragged and unpadded).
@@ -381,7 +385,9 @@ size_t bias_sums_bytes(const Geom &g, int T) { return (size_t)((T + 15) / 16) * 
 
 size_t gemm_fused_workspace_bytes(const Geom &g, int T)
 {
-    return with_padding(layout_of<FusedOp>(g, T, false), g, T, 1, 2);
+    Layout l = layout_of<FusedOp>(g, T, false);
+    take_padded(l, g, T, 1, 2);
+    return l.size();
 }
 
 cudaError_t launch_gemm_fused(const Geom &g, const LayerWeights &w, const uint16_t *x, int T, const EpilogueArgs &ep,
@@ -399,7 +405,9 @@ cudaError_t launch_gemm_fused(const Geom &g, const LayerWeights &w, const uint16
 
 size_t glu_gemm_workspace_bytes(const Geom &g, int T)
 {
-    return with_padding(layout_of<GatedOp>(g, T, false), g, T, 1, 1);
+    Layout l = layout_of<GatedOp>(g, T, false);
+    take_padded(l, g, T, 1, 1);
+    return l.size();
 }
 
 cudaError_t launch_glu_gemm(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x, int T,
@@ -419,7 +427,9 @@ size_t gemm_fused_grad_workspace_bytes(const Geom &g, int T)
 {
     Layout l = layout_of<FusedOp>(g, T, true);
     l.take(bias_sums_bytes(g, T));
-    return with_padding(l, g, T, 2, 2) + scaled_bytes(g, T, 1);
+    take_padded(l, g, T, 2, 2);
+    take_scaled(l, g, T, 1);
+    return l.size();
 }
 
 cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const uint16_t *x, const uint16_t *gy, int T,
@@ -453,7 +463,10 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
 
 size_t glu_grad_workspace_bytes(const Geom &g, int T)
 {
-    return with_padding(layout_of<GatedOp>(g, T, true), g, T, 2, 3) + scaled_bytes(g, T, 2);
+    Layout l = layout_of<GatedOp>(g, T, true);
+    take_padded(l, g, T, 2, 3);
+    take_scaled(l, g, T, 2);
+    return l.size();
 }
 
 cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const LayerWeights &up, const uint16_t *x,
@@ -482,7 +495,9 @@ size_t input_grad_workspace_bytes(const Geom &g, int T)
 {
     Layout l;
     l.end = back_plan_bytes(g, 1, T);
-    return with_padding(l, g, T, 1, 1) + scaled_bytes(g, T, 1);
+    take_padded(l, g, T, 1, 1);
+    take_scaled(l, g, T, 1);
+    return l.size();
 }
 
 cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16_t *gy, int T, uint16_t *gx, void *ws,

@@ -1,0 +1,146 @@
+"""Layer operators on the GPU at their edges: a workspace shared by any
+sequence of calls, addresses of any alignment that the header allows, values
+near the ends of binary16's range."""
+import numpy as np
+import pytest
+import torch
+
+import additive_quantized_matmul_b200 as aq
+import layer_ref as lr
+from aqtest import CANARY, guarded, guards_intact, to_f16, workspace
+from test_gpu_layer_ops import Case, acts, fenced, half
+
+pytestmark = pytest.mark.gpu
+
+COUNTERS = slice(16, 16 + 4 * 1024)
+
+
+class Block:
+    """Two layers of one shape with random codes, and a call of every entry
+    point that takes a workspace: calls() gives (name, size, run(ws) -> outputs
+    filled with a canary before the call)."""
+
+    def __init__(self, out, inp, K, B, seed):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed)
+        self.out, self.inp = out, inp
+        self.d = aq.LayerDesc.make(out, inp, K, B)
+        self.w = []
+        for _ in range(2):
+            codes = torch.randint(0, 1 << B, (out, inp // 8, K), device="cuda", generator=gen, dtype=torch.int32)
+            codes = codes.to(torch.uint8) if B == 8 else codes.to(torch.int16)
+            packed = torch.empty(aq.aq_packed_codes_bytes(self.d), dtype=torch.uint8, device="cuda")
+            aq.aq_pack_codes(self.d, codes, packed)
+            books = (torch.randn((K, 1 << B, 8), device="cuda", generator=gen) * 0.02).half()
+            scales = (torch.rand(out, device="cuda", generator=gen) + 0.5).half()
+            self.w.append((packed, books, scales))
+        self.weights = [aq.Weights.make(*w) for w in self.w]
+        self.gen = gen
+
+    def halves(self, rows, n, sigma=1.0):
+        return (torch.randn((rows, n), device="cuda", generator=self.gen) * sigma).half()
+
+    def calls(self, T, batch):
+        d, w, (gate, up), out, inp = self.d, self.w[0], self.weights, self.out, self.inp
+        x, gy, xb, res = self.halves(inp, T), self.halves(out, T, 0.1), self.halves(inp, batch), self.halves(out, T)
+
+        def fresh(*shapes):
+            return [torch.full(s, CANARY, dtype=torch.int16, device="cuda").view(torch.float16) for s in shapes]
+
+        def run(fn, shapes, call):
+            def go(ws):
+                outs = fresh(*shapes)
+                call(outs, ws)
+                return outs
+            return go
+
+        def entry(name, size, shapes, call):
+            return name, size, run(name, shapes, call)
+
+        bias = torch.empty(out, dtype=torch.float32, device="cuda")
+
+        def fused_grad(o, ws):
+            bias.fill_(7.25)
+            aq.aq_gemm_fused_grad(d, *w, x, gy, T, o[0], bias, o[1], ws, activation=4)
+            o.append(bias.clone())
+
+        return [
+            entry("input_grad", aq.aq_input_grad_workspace_bytes(d, T), [(inp, T)],
+                  lambda o, ws: aq.aq_input_grad(d, *w, gy, T, o[0], ws)),
+            entry("gemm", aq.aq_gemm_workspace_bytes(d, T), [(out, T)],
+                  lambda o, ws: aq.aq_gemm(d, *w, x, T, o[0], ws)),
+            entry("glu_grad", aq.aq_glu_grad_workspace_bytes(d, T), [(out, T), (out, T), (inp, T)],
+                  lambda o, ws: aq.aq_glu_grad(d, gate, up, x, gy, T, 4, *o, ws)),
+            entry("gemv", aq.aq_gemv_workspace_bytes(d, batch), [(out, batch)],
+                  lambda o, ws: aq.aq_gemv(d, *w, xb, batch, o[0], ws)),
+            entry("fused_grad", aq.aq_gemm_fused_grad_workspace_bytes(d, T), [(out, T), (inp, T)], fused_grad),
+            entry("gemm_fused", aq.aq_gemm_fused_workspace_bytes(d, T), [(out, T)],
+                  lambda o, ws: aq.aq_gemm_fused(d, *w, x, T, o[0], ws, residual=res)),
+            entry("gemv_fused", aq.aq_gemv_workspace_bytes(d, batch), [(out, batch)],
+                  lambda o, ws: aq.aq_gemv_fused(d, *w, xb, batch, o[0], ws, activation=4)),
+            entry("glu_gemm", aq.aq_glu_gemm_workspace_bytes(d, T), [(out, T)],
+                  lambda o, ws: aq.aq_glu_gemm(d, gate, up, x, T, 4, o[0], ws)),
+            entry("glu_gemv", aq.aq_glu_gemv_workspace_bytes(d, batch), [(out, batch)],
+                  lambda o, ws: aq.aq_glu_gemv(d, gate, up, xb, batch, 4, o[0], ws)),
+        ]
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8), (8, 8)])
+@pytest.mark.parametrize("out,inp,T,batch", [(11008, 4096, 2048, 1), (4096, 11008, 2047, 1), (4096, 4096, 45, 4),
+                                             (11008, 4096, 1, 16), (1000, 1032, 333, 2)])
+def test_one_workspace_for_any_sequence_of_calls(K, B, out, inp, T, batch):
+    """Every call, on a workspace that every other call used before it, gives
+    the bits it gives on a workspace of its own, and leaves the arrival
+    counters at zero."""
+    calls = Block(out, inp, K, B, 5).calls(T, batch)
+    alone = {}
+    for name, size, go in calls:
+        ws = workspace(size)
+        alone[name] = [o.view(torch.int16) if o.dtype == torch.float16 else o for o in go(ws)]
+        torch.cuda.synchronize()
+        assert aq.aq_workspace_status(ws) == 0
+    shared = workspace(max(size for _, size, _ in calls))
+    order = [*calls, *reversed(calls)]
+    for name, _, go in order:
+        got = go(shared)
+        torch.cuda.synchronize()
+        assert int(shared[COUNTERS].max()) == 0, f"{name} left a counter"
+        for i, (a, b) in enumerate(zip(got, alone[name])):
+            a = a.view(torch.int16) if a.dtype == torch.float16 else a
+            assert torch.equal(a, b), f"{name} output {i}"
+    assert aq.aq_workspace_status(shared) == 0
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("T", [1, 5, 40, 77])
+def test_training_step_twice_on_one_workspace(K, B, T):
+    """A block's forward and backward, twice on one workspace, the outputs
+    refilled with canaries between: each step of the second pass is held to its
+    own error on the values it was given."""
+    ff = Case(520, 264, K, B, 60 + T, layers=2)
+    down = Case(264, 520, K, B, 61 + T)
+    x, gy = acts(264, T, 1), acts(264, T, 2, 0.1)
+    sizes = [aq.aq_glu_gemm_workspace_bytes(ff.desc, T), aq.aq_gemm_fused_workspace_bytes(down.desc, T),
+             aq.aq_glu_grad_workspace_bytes(ff.desc, T), aq.aq_input_grad_workspace_bytes(down.desc, T),
+             aq.aq_gemm_workspace_bytes(down.desc, T)]
+    ws = workspace(max(sizes))
+    xd, gyd = fenced(x), fenced(gy)
+    for _ in range(2):
+        (h, y, z, gh, gg, gu, gx) = (guarded(r * T) for r in (520, 264, 264, 520, 520, 520, 264))
+        aq.aq_glu_gemm(ff.desc, *ff.weights, xd, T, 4, h[1], ws)
+        aq.aq_gemm_fused(*down.w(), h[1], T, y[1], ws, residual=xd)
+        aq.aq_input_grad(*down.w(), gyd, T, gh[1], ws)
+        aq.aq_glu_grad(ff.desc, *ff.weights, xd, gh[1], T, 4, gg[1], gu[1], gx[1], ws)
+        aq.aq_gemm(*down.w(), h[1], T, z[1], ws)
+    torch.cuda.synchronize()
+    assert aq.aq_workspace_status(ws) == 0 and int(ws[COUNTERS].max()) == 0
+    assert all(guards_intact(b[0]) for b in (h, y, z, gh, gg, gu, gx))
+    H, GH, GG, GU = (half(b[1], 520, T) for b in (h, gh, gg, gu))
+    lr.check(H, lr.glu(*ff.refs, x, "silu"), "h")
+    lr.check(half(y[1], 264, T), lr.fused(down.refs[0], H, "none", None, x), "y")
+    lr.check(half(z[1], 264, T), lr.fused(down.refs[0], H, "none"), "plain product")
+    lr.check(GH, down.refs[0].back(gy), "gh")
+    wg, wu = lr.glu_grad(*ff.refs, x, GH, "silu")
+    lr.check(GG, wg, "grad_gate")
+    lr.check(GU, wu, "grad_up")
+    lr.check(half(gx[1], 264, T), ff.refs[0].back(GG, [(ff.refs[1], GU)]), "grad_x")
