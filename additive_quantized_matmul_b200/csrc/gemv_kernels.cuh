@@ -119,7 +119,8 @@ __device__ __forceinline__ void store_one(const Out &out, int row, int batch, in
 // ([rows][batch], rows from row0), rounds once to binary16 and stores it.
 // s_sc: the block's scales in shared memory (or null: read them here).
 // Batch a multiple of 4: one row, one 8-byte store; batch 1: four rows,
-// one 8-byte scale read and one 8-byte store.
+// one 8-byte scale read (where the scales start on such a boundary) and one
+// 8-byte store.
 __device__ __forceinline__ void finish_store4(const Geom &L, int row0, int idx, int batch, float4 acc,
                                               const uint16_t *__restrict__ scales, const float *s_sc,
                                               uint16_t *__restrict__ y)
@@ -138,10 +139,13 @@ __device__ __forceinline__ void finish_store4(const Geom &L, int row0, int idx, 
         if (s_sc) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) sc[c] = s_sc[idx + c];
-        } else if (scales) {
+        } else if (scales && (reinterpret_cast<uintptr_t>(scales) & 7u) == 0) {
             const uint2 w = *reinterpret_cast<const uint2 *>(scales + row0 + idx);  // row0 + idx: a multiple of 4
             const float2 lo = h2f2(w.x), hi = h2f2(w.y);
             sc[0] = lo.x, sc[1] = lo.y, sc[2] = hi.x, sc[3] = hi.y;
+        } else if (scales) {  // on a 2-byte boundary, as the entry points allow
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[c] = __half2float(__ushort_as_half(scales[row0 + idx + c]));
         }
         *reinterpret_cast<uint2 *>(y + row0 + idx) =
             make_uint2(f2h2(sc[0] * v[0], sc[1] * v[1]), f2h2(sc[2] * v[2], sc[3] * v[3]));

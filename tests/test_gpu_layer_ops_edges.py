@@ -144,3 +144,33 @@ def test_training_step_twice_on_one_workspace(K, B, T):
     lr.check(GG, wg, "grad_gate")
     lr.check(GU, wu, "grad_up")
     lr.check(half(gx[1], 264, T), ff.refs[0].back(GG, [(ff.refs[1], GU)]), "grad_x")
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8), (1, 8), (2, 16), (8, 8)])
+@pytest.mark.parametrize("inp", [264, 1032, 2056, 4096, 4616, 8200])
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_plain_products_take_scales_at_any_even_address(K, B, inp, offset):
+    """Scales that start 2, 4 or 6 bytes past an 8-byte boundary: the bits of
+    aligned ones, whether the table kernel's splits (one per 512 features of 2x8
+    layers, 1024 of 1x8) are summed from L2 (2 to 8) or staged."""
+    b = Block(300, inp, K, B, 7)
+    packed, books, scales = b.w[0]
+    shifted = torch.full((300 + 8,), float("nan"), dtype=torch.float16, device="cuda")[offset:offset + 300]
+    shifted.copy_(scales)
+    assert shifted.data_ptr() % 8 == 2 * offset
+    for n in (1, 2, 8, 40):
+        x = b.halves(inp, n)
+        fns = [(aq.aq_gemm, aq.aq_gemm_workspace_bytes)]
+        if n <= 16:
+            fns += [(aq.aq_gemv, aq.aq_gemv_workspace_bytes), (aq.aq_gemv_ordered, aq.aq_gemv_workspace_bytes),
+                    (aq.aq_gemv_noalloc, None)]
+        for fn, size in fns:
+            got = []
+            for s in (scales, shifted):
+                full, y = guarded(300 * n)
+                ws = [] if size is None else [workspace(size(b.d, n))]
+                fn(b.d, packed, books, s, x, n, y, *ws)
+                torch.cuda.synchronize()
+                assert guards_intact(full)
+                got.append(y.clone())
+            assert torch.equal(*got), (fn.__name__, n)
