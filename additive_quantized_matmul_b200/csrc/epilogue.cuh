@@ -46,7 +46,7 @@ __device__ __forceinline__ float act_value(const ActParams &k, float v, float &s
         return (k.relu && v < 0.f) ? 0.f : v;  // a NaN stays one
     } else if constexpr (F == kActLogistic) {
         constexpr float kLog2E = 1.4426950408889634f;
-        const float v2 = v * v;
+        const float v2 = fminf(v * v, 1e30f);  // finite: 0 times it stays 0 where v is infinite
         float e, p;
         // 1 / (1 + 2^(-log2(e) a)): 0 where the power is infinite
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2E * v * fmaf(k.k2, v2, k.k1)));

@@ -174,3 +174,50 @@ def test_plain_products_take_scales_at_any_even_address(K, B, inp, offset):
                 assert guards_intact(full)
                 got.append(y.clone())
             assert torch.equal(*got), (fn.__name__, n)
+
+
+def _same_kind(got, want):
+    """NaN, +inf, -inf and finite values in the same places."""
+    got = got.astype(np.float64)
+    kinds = [(np.isnan(a), np.isposinf(a), np.isneginf(a)) for a in (got, want)]
+    return all(np.array_equal(a, b) for a, b in zip(*kinds))
+
+
+@pytest.mark.parametrize("n", [2, 6, 40])
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8), (8, 8)])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_an_infinity_becomes_what_the_formula_makes_of_it(K, B, n, kind):
+    """One token with an infinity, another with a NaN: the infinite token's
+    rows are +inf, -inf or NaN as the formula has them in IEEE arithmetic (z is
+    infinite of the sign of the weight that meets the infinity), the others
+    keep their bits."""
+    c = Case(72, 264, K, B, 31, layers=2)
+    x = acts(264, n, 1)
+    clean = (c.fused(x, kind), c.glu(x, kind))
+    bad = x.copy()
+    bad[70, 0] = np.float16(np.inf)
+    bad[5, n - 1] = np.float16(np.nan)
+    got = (c.fused(bad, kind), c.glu(bad, kind))
+    with np.errstate(invalid="ignore", over="ignore"):
+        z = [r.s * r.W[:, 70] * np.inf for r in c.refs]
+        a = lr.act(kind, z[0])[0]
+        want = (a, a * z[1])
+    for g, w, k in zip(got, want, clean):
+        assert _same_kind(g[:, 0], w)
+        if kind != "relu":
+            assert not np.isfinite(g[:, 0].astype(np.float64)).any()
+        assert np.isnan(g[:, n - 1].astype(np.float64)).all()
+        assert np.array_equal(g[:, 1:n - 1].view(np.uint16), k[:, 1:n - 1].view(np.uint16))
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8), (1, 8)])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_an_infinity_in_the_only_token(K, B, kind):
+    c = Case(72, 264, K, B, 31, layers=2)
+    x = acts(264, 1, 1)
+    x[70, 0] = np.float16(np.inf)
+    with np.errstate(invalid="ignore", over="ignore"):
+        z = [r.s * r.W[:, 70] * np.inf for r in c.refs]
+        a = lr.act(kind, z[0])[0]
+        assert _same_kind(c.fused(x, kind)[:, 0], a)
+        assert _same_kind(c.glu(x, kind)[:, 0], a * z[1])
