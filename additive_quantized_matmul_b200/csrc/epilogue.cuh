@@ -42,8 +42,8 @@ template <int F>
 __device__ __forceinline__ float act_value(const ActParams &k, float v, float &slope)
 {
     if constexpr (F == kActLinear) {
-        slope = (k.relu && !(v > 0.f)) ? 0.f : 1.f;
-        return (k.relu && v < 0.f) ? 0.f : v;  // a NaN stays one
+        slope = !k.relu || v > 0.f ? 1.f : v <= 0.f ? 0.f : v;
+        return (k.relu && v < 0.f) ? 0.f : v;  // (a NaN stays one in both)
     } else if constexpr (F == kActLogistic) {
         constexpr float kLog2E = 1.4426950408889634f;
         const float v2 = fminf(v * v, 1e30f);  // finite: 0 times it stays 0 where v is infinite

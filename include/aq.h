@@ -347,7 +347,7 @@ aq_status aq_param_grad(const aq_layer_desc *desc, const void *packed, const uin
  * result is rounded once where it is written.
  */
 
-/* Activation functions; z in fp32, NaN stays NaN. */
+/* Activation functions; z in fp32, NaN stays NaN, in the slopes too. */
 typedef enum {
     AQ_ACT_NONE = 0,      /* z                                                   */
     AQ_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0                             */

@@ -221,3 +221,21 @@ def test_an_infinity_in_the_only_token(K, B, kind):
         a = lr.act(kind, z[0])[0]
         assert _same_kind(c.fused(x, kind)[:, 0], a)
         assert _same_kind(c.glu(x, kind)[:, 0], a * z[1])
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("T", [1, 5, 40, 520])
+@pytest.mark.parametrize("kind", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slopes_keep_a_nan(K, B, T, kind):
+    """A NaN in one token's activations: that token's gradients are NaN, the
+    others keep their bits."""
+    c = Case(72, 264, K, B, 33, layers=2)
+    x, gy = acts(264, T, 1), acts(72, T, 2, 0.1)
+    bad = x.copy()
+    bad[9, T - 1] = np.float16(np.nan)
+    with_bias = acts(72, 1, 3).ravel()
+    clean = c.fused_grad(x, gy, kind, with_bias, want_bias=False)[0], *c.glu_grad(x, gy, kind)[:2]
+    got = c.fused_grad(bad, gy, kind, with_bias, want_bias=False)[0], *c.glu_grad(bad, gy, kind)[:2]
+    for g, k in zip(got, clean):
+        assert np.isnan(g[:, T - 1].astype(np.float64)).all()
+        assert np.array_equal(g[:, :T - 1].view(np.uint16), k[:, :T - 1].view(np.uint16))
