@@ -556,6 +556,15 @@ gemv_lut_kernel(Geom L, const __grid_constant__ Out out, const uint16_t *__restr
     const float bound = 8.f * __half2float(__ushort_as_half((unsigned short)s_max[0])) *
                         __half2float(__ushort_as_half((unsigned short)s_max[1]));
     const bool exact = !(bound < 65504.f);
+    // the fused and gated forms store the entries times the power of two that
+    // brings the bound to 2^14 .. 2^15 (never less than 1), so that those of
+    // small activations do not sink below binary16's normal range; the rows'
+    // fp32 sums are divided by it again, both exact
+    float up = 1.f, down = 1.f;
+    if constexpr (Out::kFused || Out::kGated) {
+        const int e = !exact && bound > 0.f ? max(0, 14 - ilogbf(bound)) : 0;  // at most 59
+        up = ldexpf(1.f, e), down = ldexpf(1.f, -e);
+    }
     if (!exact) {
         // warp w fills the codeword octets n = w + 16 i (codeword kc = 8 n +
         // 0..7, kc = k*256 + c) for every group of the CTA
@@ -590,8 +599,8 @@ gemv_lut_kernel(Geom L, const __grid_constant__ Out out, const uint16_t *__restr
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     // v[s] is word l = gid + 8 s: groups (gid + 8 s, + 32) of codeword kc + b
-                    const uint32_t v[4] = {f2h2(lo0[b], hi0[b]), f2h2(lo0[2 + b], hi0[2 + b]),
-                                           f2h2(lo1[b], hi1[b]), f2h2(lo1[2 + b], hi1[2 + b])};
+                    const uint32_t v[4] = {f2h2(up * lo0[b], up * hi0[b]), f2h2(up * lo0[2 + b], up * hi0[2 + b]),
+                                           f2h2(up * lo1[b], up * hi1[b]), f2h2(up * lo1[2 + b], up * hi1[2 + b])};
                     uint32_t r[4], w[4];
 #pragma unroll
                     for (int s2 = 0; s2 < 4; ++s2) r[s2] = (t4 & 1) ? v[(s2 + 1) & 3] : v[s2];
@@ -668,7 +677,7 @@ gemv_lut_kernel(Geom L, const __grid_constant__ Out out, const uint16_t *__restr
                     acc[r] = a;
                 }
             }
-            const float v = warp_reduce8(acc, lane);
+            const float v = down * warp_reduce8(acc, lane);
             const int row = (rt0 + warp + kLutWarps * i) * 8 + reduced_row_of_lane(lane);
             if ((lane & 3) == 0) {
                 if (one_slot<Out>()) {

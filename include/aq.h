@@ -386,7 +386,9 @@ typedef struct {
  * bias off a 2-byte boundary.
  * With one or two 8-bit codebooks at batch 1 the products come from lookup
  * tables, as in aq_gemv (the layer's sums of codewords enter unrounded, each
- * table entry rounded to binary16); the looked-up entries are added in fp32.
+ * table entry rounded to binary16, times a power of two that keeps the entries
+ * of small activations in the normal range); the looked-up entries are added in
+ * fp32.
  * For T not a multiple of 8 aq_gemm_fused makes three launches (rows that TMA
  * can address are built in the workspace and copied back), else one.
  */

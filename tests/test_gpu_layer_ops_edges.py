@@ -239,3 +239,41 @@ def test_slopes_keep_a_nan(K, B, T, kind):
     for g, k in zip(got, clean):
         assert np.isnan(g[:, T - 1].astype(np.float64)).all()
         assert np.array_equal(g[:, :T - 1].view(np.uint16), k[:, :T - 1].view(np.uint16))
+
+
+def _step2(v):
+    """Mean square error of rounding v to binary16: a twelfth of the step's square."""
+    e = np.maximum(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -40))), -14)
+    return np.where(v == 0, 0.0, 4.0 ** (e - 10) / 12)
+
+
+def _table_sums(ref, layer, x):
+    """s (sum of codewords) x, unrounded, and the mean square error that
+    rounding each table entry <codeword, x_g> once to 11 bits makes of it."""
+    K = layer.spec.num_codebooks
+    cb = lr.f64(layer.codebooks).reshape(K, -1, 8)
+    codes = layer.codes.reshape(layer.spec.out_features, -1, K).astype(np.int64)
+    xg = x.astype(np.float64).reshape(-1, 8)
+    total = var = 0.0
+    for k in range(K):
+        entries = np.take_along_axis(np.einsum("cj,gj->gc", cb[k], xg), codes[:, :, k].T, axis=1)  # [groups][rows]
+        total = total + entries.sum(0)
+        steps = np.where(entries == 0, 0.0, 4.0 ** (np.floor(np.log2(np.abs(entries) + (entries == 0))) - 10) / 12)
+        var = var + steps.sum(0)
+    return ref.s * total, ref.s ** 2 * var
+
+
+@pytest.mark.parametrize("K,B", [(2, 8), (1, 8)])
+@pytest.mark.parametrize("sigma", [1.0, 1e-2, 1e-3, 1e-4, 1e-6])
+def test_table_entries_of_small_activations_keep_their_bits(K, B, sigma):
+    """One token, 8-bit codebooks: the root mean square error over 2048 rows is
+    that of one 11-bit rounding per table entry and one of the result, whatever
+    the size of the activations.  It is estimated from 2048 rows (2 % spread);
+    binary16 additions of four entries would make it 1.7 times as large."""
+    out, inp = 2048, 4096
+    c = Case(out, inp, K, B, 15, layers=2, scale=min(1 / sigma, 16000.0))
+    x = acts(inp, 1, 1, sigma)
+    (zg, vg), (zu, vu) = (_table_sums(r, L, x) for r, L in zip(c.refs, c.layers))
+    for got, want, var in ((c.fused(x, "none"), zg, vg), (c.glu(x, "none"), zg * zu, zu ** 2 * vg + zg ** 2 * vu)):
+        err = got[:, 0].astype(np.float64) - want
+        assert np.sqrt((err ** 2).mean()) <= 1.2 * np.sqrt((var + _step2(want)).mean())
