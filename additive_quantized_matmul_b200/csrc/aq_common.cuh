@@ -52,7 +52,9 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 
 // Workspace layout, the same for every entry point, so that one workspace
 // serves any sequence of calls on a stream: status word at byte 0
-// (AQ_ERR_TIMEOUT when a bounded wait gave up); split-K arrival counters in
+// (AQ_ERR_TIMEOUT when a bounded wait gave up); at byte 4 the largest scaled
+// gradient of a backward pass under way (bits of a float, zero between
+// calls); split-K arrival counters in
 // a fixed area of kWsMaxCounters words from byte 16, which only counters
 // ever use and every call leaves at zero; the entry point's own data
 // (split-K partial sums, tables) from kWsData on.  A plan splits a sum
@@ -60,6 +62,8 @@ inline size_t align16(size_t v) { return (v + 15) / 16 * 16; }
 constexpr size_t kWsHeader = 16;
 constexpr int kWsMaxCounters = 1024;
 constexpr size_t kWsData = kWsHeader + sizeof(unsigned) * kWsMaxCounters;
+// (the word at byte 4)
+inline unsigned *ws_top(void *ws) { return reinterpret_cast<unsigned *>(ws) + 1; }
 
 // Atomic add with release and acquire semantics at GPU scope; returns the
 // old value.

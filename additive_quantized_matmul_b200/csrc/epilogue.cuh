@@ -113,35 +113,25 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N])
 __device__ __forceinline__ float half_bits_to_float(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 __device__ __forceinline__ uint16_t float_to_half_bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
 
-// Largest |v| (as the bits of a binary16; NaN above infinity) of this
-// thread's share of v[0 .. n), `threads` threads in all.
-__device__ __forceinline__ uint32_t absmax_share(const uint16_t *__restrict__ v, int n, int thread, int threads)
+// Largest finite magnitude of pairs of binary16 values, per half; and the float
+// it stands for in a row of scale s (0 where s is not finite: the whole row's
+// products are not, whatever is made of them).
+__device__ __forceinline__ void finite_absmax_h2(uint32_t &m, uint32_t w)
 {
-    uint32_t m = 0;
-    // 16-byte pieces between the ragged ends (v has 2-byte alignment)
-    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(v) & 15)) & 15) / 2);
-    const int nv = (n - head) / 8;
-    const uint4 *v4 = reinterpret_cast<const uint4 *>(v + head);
-#pragma unroll 8
-    for (int i = thread; i < nv; i += threads) {
-        const uint4 q = __ldg(v4 + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
-    }
-    if (thread < head) m = max(m, (uint32_t)v[thread] & 0x7fffu);
-    if (head + nv * 8 + thread < n && thread < 8) m = max(m, (uint32_t)v[head + nv * 8 + thread] & 0x7fffu);
-    return m;
+    const __half2 a = __habs2(*reinterpret_cast<const __half2 *>(&w));
+    uint32_t b = *reinterpret_cast<const uint32_t *>(&a);
+    b &= __hlt2_mask(a, __half2half2(__ushort_as_half(0x7c00)));  // false for infinities and NaN
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2 *>(&m), *reinterpret_cast<const __half2 *>(&b));
+    m = *reinterpret_cast<const uint32_t *>(&r);
 }
-
-// The transposed product multiplies the row scales into one of its binary16
-// operands, divided by 2^E, the power of two just above the largest |scale|
-// (its binary16 bits `m`): no product overflows, and uniformly small scales
-// lose no bits.  0 if every scale is zero; 2^16 covers every finite value, and
-// infinities and NaN go through.
-__device__ __forceinline__ int scale_exponent(uint32_t m)
+__device__ __forceinline__ void finite_absmax_h8(uint32_t &m, uint4 v)
 {
-    return m >= 0x7c00u ? 16 : m ? ilogbf(half_bits_to_float((uint16_t)m)) + 1 : 0;
+    finite_absmax_h2(m, v.x), finite_absmax_h2(m, v.y), finite_absmax_h2(m, v.z), finite_absmax_h2(m, v.w);
+}
+__device__ __forceinline__ float scaled_top(uint32_t m, float s)
+{
+    const float2 f = h2f2(m);
+    return fabsf(s) < 65536.f ? fabsf(s) * fmaxf(f.x, f.y) : 0.f;
 }
 
 // One layer's stored weights on the device.

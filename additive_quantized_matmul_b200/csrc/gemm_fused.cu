@@ -28,7 +28,7 @@ namespace aqk {
 // aligned piece of its own, m the same for the whole row, so a lane reads one
 // aligned piece, gets the next from its neighbour and shifts; the up to seven
 // elements at either end of a row go singly.  With scales (a whole launch's
-// arrays are multiplied, by 2^-E alone where an array has none) each element
+// arrays are multiplied, by 2^-E alone where an array has none) each product
 // is rounded once.  Bound by the latency of its round trips: two scaled arrays of
 // 11008 rows and 2048 tokens (90 MB read, 90 MB written) 42 us with cold caches,
 // which is why aligned ones have scale_rows_kernel.
@@ -39,6 +39,7 @@ struct RowCopies {
     aqh::RowCopy job[aqh::kMaxRowCopies];
     int jobs;
     float *factor;  // with scales: receives 2^E
+    unsigned *top;  // with scales: the largest product (bits of a float)
 };
 
 // Bytes m .. m + 15 of the 32 bytes (a, b); m even, the same in every lane.
@@ -56,20 +57,49 @@ __device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int m)
                       __funnelshift_r(w[3], w[4], sh));
 }
 
-// Every CTA looks through all the scales.
-__device__ __forceinline__ int largest_scale_exponent(const RowCopies &jobs)
+// *top = the largest finite |scales[r] src[r][t]| over the jobs, all of as many
+// rows (*top zero before).  A warp takes 4 KiB of a row at a time, its aligned
+// pieces by 16 bytes, the up to seven elements at either end singly.  One pass
+// over the gradients, bound by HBM or, for short ones, the launch.
+constexpr int kMaxPieces = 256;  // pieces of a row per warp
+
+__global__ void __launch_bounds__(kCopyThreads) scaled_max_kernel(const __grid_constant__ RowCopies jobs, int T)
 {
-    __shared__ uint32_t s_max;
-    if (threadIdx.x == 0) s_max = 0;
-    __syncthreads();
-    uint32_t m = 0;
-    for (int j = 0; j < jobs.jobs; ++j)
-        m = max(m, jobs.job[j].scales ? absmax_share(jobs.job[j].scales, jobs.job[j].rows, threadIdx.x, kCopyThreads)
-                                      : 0x3c00u);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) atomicMax(&s_max, m);
-    __syncthreads();
-    return scale_exponent(s_max);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, rows = jobs.job[0].rows;
+    const unsigned shares = ((unsigned)T + 8 * kMaxPieces - 1) / (8 * kMaxPieces);
+    const int step = gridDim.x * (kCopyThreads / 32);
+    float m = 0.f;
+    for (int j = 0; j < jobs.jobs; ++j) {
+        const aqh::RowCopy &c = jobs.job[j];
+        for (long i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); i < (long)rows * shares; i += step) {
+            const int r = shares == 1 ? (int)i : (int)(i / shares);
+            const int t0 = shares == 1 ? 0 : (int)(i % shares) * (8 * kMaxPieces);
+            const int n = min(8 * kMaxPieces, T - t0);
+            const uint16_t *src = c.src + (size_t)r * c.src_pitch + t0;
+            const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / 2);
+            const int pieces = (n - head) / 8;
+            const uint4 *from = reinterpret_cast<const uint4 *>(src + head);
+            uint32_t h = 0;
+#pragma unroll
+            for (int q = 0; q < kMaxPieces / 32; ++q)
+                if (32 * q + lane < pieces) finite_absmax_h8(h, __ldg(from + 32 * q + lane));
+            const int e = lane < 8 ? lane : head + 8 * pieces + lane - 8;
+            if (lane < 8 ? lane < head : lane < 16 && e < n) finite_absmax_h2(h, src[e]);
+            m = fmaxf(m, scaled_top(h, c.scales ? half_bits_to_float(__ldg(c.scales + r)) : 1.f));
+        }
+    }
+    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == 0) atomicMax(jobs.top, w);
+}
+
+// E of the largest product: 2^14 <= top / 2^E < 2^15, so that none overflows, nor
+// loses bits that matter beside the largest one (2^-25 is 2^-39 of it).  |E| < 64.
+__device__ __forceinline__ int scale_exponent(const RowCopies &jobs)
+{
+    const float m = __uint_as_float(__ldcg(jobs.top));
+    return m > 0.f ? ilogbf(m) - 14 : 0;
 }
 
 __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
@@ -80,7 +110,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     float inv = 1.f;
     if (jobs.factor) {  // some job has scales
-        const int e = largest_scale_exponent(jobs);
+        const int e = scale_exponent(jobs);
         inv = ldexpf(1.f, -e);
         if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *jobs.factor = ldexpf(1.f, e);
     }
@@ -135,12 +165,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
 
 // The same for scaled rows of T = pitch, a multiple of 8: every piece is aligned
 // in both arrays.  A warp takes 2 KiB of a row, the next row's share requested
-// before this one's is multiplied, the first before the scales are looked
-// through; 48 registers leave room for five CTAs an SM (64 and four above).
-// Beside copy_rows_kernel, whole calls: backward of a gated block, 1x16, 2 x
-// 11008 rows, 2048 tokens 765 -> 747 us alone (793 -> 791 in series, where power
-// bounds it); input gradients of 11008 rows, 1024 tokens 111.5 -> 109.2, of 4096
-// rows, 512 tokens 36.1 -> 35.2.
+// before this one's is multiplied; 48 registers leave room for five CTAs an SM
+// (64 and four above).
 __global__ void __launch_bounds__(kCopyThreads, 5) scale_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
 {
     constexpr int kN = kCopyPieces / 32;
@@ -158,7 +184,7 @@ __global__ void __launch_bounds__(kCopyThreads, 5) scale_rows_kernel(const __gri
     int r = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
     uint4 a[kN] = {}, b[kN] = {};
     if (r < c.rows) read(r, a);
-    const int e = largest_scale_exponent(jobs);
+    const int e = scale_exponent(jobs);
     const float inv = ldexpf(1.f, -e);
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *jobs.factor = ldexpf(1.f, e);
     for (; r < c.rows; r += step) {
@@ -243,26 +269,44 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const uint16_t *__rest
 namespace aqh {
 using namespace aqk;
 
-cudaError_t copy_rows(const RowCopy *jobs, int n, int T, float *factor, cudaStream_t s)
+static RowCopies all_jobs(const RowCopy *jobs, int n)
 {
     RowCopies all{};
     all.jobs = n;
-    for (int i = 0; i < n; ++i)
-        if (jobs[i].scales) all.factor = factor;
-    int rows = 0;
-    for (int i = 0; i < n; ++i) {
-        all.job[i] = jobs[i];
-        rows = std::max(rows, jobs[i].rows);
-    }
+    for (int i = 0; i < n; ++i) all.job[i] = jobs[i];
+    return all;
+}
+
+// `per_sm` CTAs an SM over `arrays` arrays, or one per eight rows
+static dim3 copy_grid(int rows, int T, int n, int arrays, int per_sm)
+{
     const unsigned pieces = (unsigned)std::max(1, (T / 8 + kCopyPieces - 1) / kCopyPieces);
-    const int share = (int)pieces * (all.factor ? n : 1);
-    auto grid = [&](int per_sm) {
-        return dim3(std::max(1, std::min((rows + 7) / 8, per_sm * kNumSMs / share + 1)), pieces, n);
-    };
-    // with scales every CTA reads all of them: one wave
-    if (all.factor && T % 8 == 0)
-        return launch_programmatic(scale_rows_kernel, grid(5), dim3(kCopyThreads), s, all, T);
-    return launch_programmatic(copy_rows_kernel, grid(all.factor ? 4 : 16), dim3(kCopyThreads), s, all, T);
+    const int share = (int)pieces * arrays;
+    return dim3(std::max(1, std::min((rows + 7) / 8, per_sm * kNumSMs / share + 1)), pieces, n);
+}
+
+cudaError_t copy_rows(const RowCopy *jobs, int n, int T, cudaStream_t s)
+{
+    int rows = 0;
+    for (int i = 0; i < n; ++i) rows = std::max(rows, jobs[i].rows);
+    return launch_programmatic(copy_rows_kernel, copy_grid(rows, T, n, 1, 16), dim3(kCopyThreads), s, all_jobs(jobs, n), T);
+}
+
+cudaError_t scale_rows(const RowCopy *jobs, int n, int T, float *factor, unsigned *top, bool known, cudaStream_t s)
+{
+    const int rows = jobs[0].rows;
+    RowCopies all = all_jobs(jobs, n);
+    all.factor = factor;
+    all.top = top;
+    if (!known) {
+        const long shares = ((long)T + 8 * kMaxPieces - 1) / (8 * kMaxPieces);
+        const unsigned ctas = (unsigned)std::min<long>(4 * kNumSMs, (rows * shares + 7) / 8);
+        const cudaError_t e = launch_programmatic(scaled_max_kernel, dim3(ctas), dim3(kCopyThreads), s, all, T);
+        if (e != cudaSuccess) return e;
+    }
+    if (T % 8 == 0)
+        return launch_programmatic(scale_rows_kernel, copy_grid(rows, T, n, n, 5), dim3(kCopyThreads), s, all, T);
+    return launch_programmatic(copy_rows_kernel, copy_grid(rows, T, n, n, 4), dim3(kCopyThreads), s, all, T);
 }
 
 namespace {
@@ -326,8 +370,8 @@ public:
         out_[nout_++] = RowCopy{p, a, rows, padded_tokens(T_), T_, nullptr};
         return p;
     }
-    cudaError_t before(cudaStream_t s) const { return nin_ ? copy_rows(in_, nin_, T_, nullptr, s) : cudaSuccess; }
-    cudaError_t after(cudaStream_t s) const { return nout_ ? copy_rows(out_, nout_, T_, nullptr, s) : cudaSuccess; }
+    cudaError_t before(cudaStream_t s) const { return nin_ ? copy_rows(in_, nin_, T_, s) : cudaSuccess; }
+    cudaError_t after(cudaStream_t s) const { return nout_ ? copy_rows(out_, nout_, T_, s) : cudaSuccess; }
 
 private:
     uint16_t *room(int rows) { return reinterpret_cast<uint16_t *>(ws_ + l_.take(padded_bytes(rows, T_))); }
@@ -347,8 +391,8 @@ void take_padded(Layout &l, const Geom &g, int T, int in_arrays, int out_arrays)
     for (int i = 0; i < out_arrays; ++i) l.take(padded_bytes(g.out, T));
 }
 
-// The gradients that the transposed product reads: as they are, or (1x16
-// layers with scales) copies multiplied by the scales, in one launch.
+// The gradients that the transposed product reads: as they are, or, of layers
+// with scales, copies multiplied by them.
 struct Scaled {
     const uint16_t *g[2];
     const float *factor;  // or null
@@ -356,18 +400,18 @@ struct Scaled {
 
 void take_scaled(Layout &l, const Geom &g, int T, int layers)
 {
-    if (!back_takes_scaled(g)) return;
     l.take(sizeof(float));
     for (int i = 0; i < layers; ++i) l.take(padded_bytes(g.out, T));
 }
 
-// `pitch`: of the gradients in memory (T where they are ragged and unpadded).
+// `pitch`: of the gradients in memory (T where they are ragged and unpadded);
+// `known`: ws_top holds the largest scaled one.
 cudaError_t scale_gradients(const Geom &g, Layout &l, char *ws, int layers, const LayerWeights *w,
-                            const uint16_t *const *grads, int T, int pitch, Scaled *out, cudaStream_t s)
+                            const uint16_t *const *grads, int T, int pitch, bool known, Scaled *out, cudaStream_t s)
 {
     *out = Scaled{{grads[0], layers > 1 ? grads[1] : grads[0]}, nullptr};
     const bool scales = w[0].scales || (layers > 1 && w[1].scales);
-    if (!back_takes_scaled(g) || (!scales && pitch == padded_tokens(T))) return cudaSuccess;
+    if (!scales && pitch == padded_tokens(T)) return cudaSuccess;
     float *factor = reinterpret_cast<float *>(ws + l.take(sizeof(float)));
     RowCopy jobs[2];
     for (int i = 0; i < layers; ++i) {
@@ -375,8 +419,9 @@ cudaError_t scale_gradients(const Geom &g, Layout &l, char *ws, int layers, cons
         jobs[i] = RowCopy{grads[i], z, g.out, pitch, padded_tokens(T), w[i].scales};
         out->g[i] = z;
     }
-    if (scales) out->factor = factor;
-    return copy_rows(jobs, layers, T, factor, s);
+    if (!scales) return copy_rows(jobs, layers, T, s);
+    out->factor = factor;
+    return scale_rows(jobs, layers, T, factor, ws_top(ws), known, s);
 }
 
 size_t bias_sums_bytes(const Geom &g, int T) { return (size_t)((T + 15) / 16) * g.out * sizeof(float); }
@@ -397,7 +442,7 @@ cudaError_t launch_gemm_fused(const Geom &g, const LayerWeights &w, const uint16
     char *base = reinterpret_cast<char *>(ws);
     Arrays a(l, base, T);
     const uint16_t *xk = a.in(x, g.in), *rk = a.in(ep.residual, g.out);
-    const FusedOp op{{w}, ep.act, ep.bias, rk, a.out(y, g.out), false, nullptr};
+    const FusedOp op{{w}, ep.act, ep.bias, rk, a.out(y, g.out), false, nullptr, nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     return e == cudaSuccess ? a.after(s) : e;
@@ -417,7 +462,7 @@ cudaError_t launch_glu_gemm(const Geom &g, const LayerWeights &gate, const Layer
     char *base = reinterpret_cast<char *>(ws);
     Arrays a(l, base, T);
     const uint16_t *xk = a.in(x, g.in);
-    const GatedOp op{{gate, up}, act, nullptr, a.out(y, g.out), nullptr};
+    const GatedOp op{{gate, up}, act, nullptr, a.out(y, g.out), nullptr, nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     return e == cudaSuccess ? a.after(s) : e;
@@ -447,7 +492,8 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
     Arrays a(l, base, T);
     const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
     uint16_t *zk = a.out(grad_z, g.out), *gxk = a.out(grad_x, g.in);
-    const FusedOp op{{w}, ep.act, ep.bias, gk, zk, true, grad_bias ? sums : nullptr};
+    const FusedOp op{{w}, ep.act, ep.bias, gk, zk, true, grad_bias ? sums : nullptr,
+                     grad_x && w.scales ? ws_top(ws) : nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     if (e == cudaSuccess && grad_bias)
@@ -455,7 +501,7 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
                                 (T + 15) / 16, g.out, grad_bias);
     if (e == cudaSuccess && grad_x) {
         Scaled z;
-        e = scale_gradients(g, l, base, 1, &w, &zk, T, padded_tokens(T), &z, s);
+        e = scale_gradients(g, l, base, 1, &w, &zk, T, padded_tokens(T), true, &z, s);
         if (e == cudaSuccess) e = launch_back(g, 1, w, z.g[0], w, nullptr, T, z.factor, gxk, ws, s);
     }
     return e == cudaSuccess ? a.after(s) : e;
@@ -478,14 +524,14 @@ cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const Layer
     Arrays a(l, base, T);
     const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
     uint16_t *ggk = a.out(grad_gate, g.out), *guk = a.out(grad_up, g.out), *gxk = a.out(grad_x, g.in);
-    const GatedOp op{{gate, up}, act, gk, ggk, guk};
+    const GatedOp op{{gate, up}, act, gk, ggk, guk, grad_x && (gate.scales || up.scales) ? ws_top(ws) : nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     if (e == cudaSuccess && grad_x) {
         const LayerWeights w[2] = {gate, up};
         const uint16_t *grads[2] = {ggk, guk};
         Scaled z;
-        e = scale_gradients(g, l, base, 2, w, grads, T, padded_tokens(T), &z, s);
+        e = scale_gradients(g, l, base, 2, w, grads, T, padded_tokens(T), true, &z, s);
         if (e == cudaSuccess) e = launch_back(g, 2, gate, z.g[0], up, z.g[1], T, z.factor, gxk, ws, s);
     }
     return e == cudaSuccess ? a.after(s) : e;
@@ -507,12 +553,9 @@ cudaError_t launch_input_grad(const Geom &g, const LayerWeights &w, const uint16
     l.end = back_plan_bytes(g, 1, T);
     char *base = reinterpret_cast<char *>(ws);
     Arrays a(l, base, T);
-    const bool scaled = back_takes_scaled(g);  // one launch pads and scales
-    const uint16_t *gk = scaled ? gy : a.in(gy, g.out);
     uint16_t *gxk = a.out(gx, g.in);
-    cudaError_t e = a.before(s);
-    Scaled z;
-    if (e == cudaSuccess) e = scale_gradients(g, l, base, 1, &w, &gk, T, scaled ? T : padded_tokens(T), &z, s);
+    Scaled z;  // (the copy of ragged rows pads them, scaled or not)
+    cudaError_t e = scale_gradients(g, l, base, 1, &w, &gy, T, T, false, &z, s);
     if (e == cudaSuccess) e = launch_back(g, 1, w, z.g[0], w, nullptr, T, z.factor, gxk, ws, s);
     return e == cudaSuccess ? a.after(s) : e;
 }

@@ -49,9 +49,9 @@
 //    runs over the layer's rows (of one or two layers, one after the other):
 //    thread t decodes chunk (row tile t/16, group t%16) and its codewords
 //    lie along M, so A is MN-major like B.  The row scale belongs to the
-//    contraction index and is multiplied, divided by 2^E (scale_exponent),
-//    into the weights or, before, into the other operand: one rounding to
-//    binary16 each; 2^E is applied to the fp32 sums.
+//    contraction index and is multiplied, divided by 2^E, into the other
+//    operand before (scale_rows in layer_ops.cuh: one rounding to binary16);
+//    2^E is applied to the fp32 sums.
 #pragma once
 
 #include <cuda.h>
@@ -140,7 +140,7 @@ __device__ __forceinline__ void widen_h8(uint4 p, float *v)
 // Where a tile's sums are written.
 struct TileOut {
     int mt, n0, T;
-    float factor;  // kTransposed: 2^E
+    float factor;  // kTransposed: 2^E, or 1
 };
 
 // ---- operators ----------------------------------------------------------------
@@ -158,7 +158,6 @@ struct TileOut {
 // y = RN16(s (W x)); T % 8 == 0.
 struct PlainOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = false;
-    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kMaps = 1, kXMaps = 1, kAhead = 4;
     static constexpr bool kPairs = false;
     LayerWeights w[1];
@@ -169,7 +168,6 @@ struct PlainOp {
 // act'(z)) and the sums of gy act'(z) over each block of 16 tokens.
 struct FusedOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = true;
-    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kXMaps = 1, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -180,6 +178,7 @@ struct FusedOp {
     uint16_t *out;         // y, or grad_z
     bool grad;
     float *sums;           // grad: [blocks of 16 tokens][out], or null
+    unsigned *top;         // grad: ws_top, takes the largest |s grad_z|; or null
 
     struct Row {
         float sc, b;
@@ -206,7 +205,8 @@ struct FusedOp {
     }
     template <int Family, bool Grad>
     __device__ __forceinline__ void apply(const Geom &L, const TileOut &o, const ActParams &k, const Row &r, int gn,
-                                          float (&v)[16], const uint4 (&x)[2], uint4 (&y0)[2], uint4 (&)[2]) const
+                                          float (&v)[16], const uint4 (&x)[2], uint4 (&y0)[2], uint4 (&)[2],
+                                          uint32_t (&m)[2]) const
     {
         float sum = 0.f;
 #pragma unroll
@@ -226,18 +226,19 @@ struct FusedOp {
                 }
             }
             y0[h] = round_h8(a);
+            if constexpr (Grad) finite_absmax_h8(m[0], y0[h]);
         }
         if constexpr (Grad) {
             const int i = row0(o) + (int)(threadIdx.x & 31);
             if (sums && i < L.out) sums[(size_t)(gn >> 4) * L.out + i] = sum;
         }
     }
+    __device__ __forceinline__ float largest(const Row &r, const uint32_t (&m)[2]) const { return scaled_top(m[0], r.sc); }
 };
 
 // Gated block: y = RN16(act(g) u), or, with gy, the gradients of g and u.
 struct GatedOp {
     static constexpr bool kGated = true, kTransposed = false, kStaged = true;
-    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 2, kXMaps = 1, kRows = 16, kPieces = 1, kOutputs = 2, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -245,6 +246,7 @@ struct GatedOp {
     int act;
     const uint16_t *gy;      // or null: forward
     uint16_t *out0, *out1;   // y, -; or grad_gate, grad_up
+    unsigned *top;           // gy: ws_top, takes the largest |s_g grad_gate|, |s_u grad_up|; or null
 
     struct Row {
         float sc;
@@ -277,7 +279,8 @@ struct GatedOp {
     }
     template <int Family, bool Grad>
     __device__ __forceinline__ void apply(const Geom &, const TileOut &, const ActParams &k, const Row &r, int,
-                                          float (&v)[16], const uint4 (&x)[1], uint4 (&y0)[1], uint4 (&y1)[1]) const
+                                          float (&v)[16], const uint4 (&x)[1], uint4 (&y0)[1], uint4 (&y1)[1],
+                                          uint32_t (&m)[2]) const
     {
         const bool hi = threadIdx.x & 16;
         float a[8], c[8], e[8];
@@ -296,25 +299,35 @@ struct GatedOp {
             }
         }
         y0[0] = round_h8(a);
-        if constexpr (Grad) y1[0] = round_h8(c);
+        if constexpr (Grad) {
+            y1[0] = round_h8(c);
+            finite_absmax_h8(m[0], y0[0]);
+            finite_absmax_h8(m[1], y1[0]);
+        }
+    }
+    __device__ __forceinline__ float largest(const Row &r, const uint32_t (&m)[2]) const
+    {
+        const bool hi = threadIdx.x & 16;
+        const float other = __shfl_xor_sync(0xffffffffu, r.sc, 16);
+        return fmaxf(scaled_top(m[0], hi ? other : r.sc), scaled_top(m[1], hi ? r.sc : other));
     }
 };
 
-// gx = RN16(sum over the layers of W^T (s gy)).  Scaled: gy comes multiplied
-// by s / 2^E, and the weights go into shared memory as they are (1x16: by
+// gx = RN16(2^E sum over the layers of W^T g), g = s gy / 2^E: the scales are in
+// g, so that the weights go into shared memory as they are (1x16: by
 // asynchronous copies; scaling them on the way through registers took 2207
-// cycles a stage against 1400); else the decoders scale the weights.
-template <bool Scaled>
+// cycles a stage against 1400, and a weight times a scale far below the largest
+// one would be subnormal).
 struct BackOp {
     static constexpr bool kGated = false, kTransposed = true, kStaged = true;
-    static constexpr bool kScaleWeights = !Scaled;
     static constexpr int kLayers = 2, kXMaps = 2, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[2];
     int layers;  // 1 or 2
     uint16_t *gx;
-    const float *factor;  // Scaled: 2^E
+    const float *factor;  // 2^E, or null: 1
+    unsigned *top;        // with factor: to be cleared
     static constexpr int act = AQ_ACT_NONE;
 
     struct Row {
@@ -331,7 +344,8 @@ struct BackOp {
     }
     template <int, bool>
     __device__ __forceinline__ void apply(const Geom &, const TileOut &, const ActParams &, const Row &r, int,
-                                          float (&v)[16], const uint4 (&)[2], uint4 (&y0)[2], uint4 (&)[2]) const
+                                          float (&v)[16], const uint4 (&)[2], uint4 (&y0)[2], uint4 (&)[2],
+                                          uint32_t (&)[2]) const
     {
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] *= r.sc;
@@ -468,6 +482,7 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
     const int r_lane = R == 32 ? lane : lane & 15, p_lane = R == 32 ? 0 : lane >> 4;
     auto box = [&](int cb, int a) { return stage + ((size_t)a * (BN / 64) + cb / 64) * (4 * kBox) + q * kBox; };
     const uint16_t *in = op.io(0);
+    uint32_t top[2] = {0u, 0u};  // Grad: largest finite results, per half
     if (in && lane == 0) {
         fence_proxy_async_smem();
         for (int cb = c; cb < end; cb += step) {
@@ -493,7 +508,7 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
             at[i] = sw128((uint32_t)r_lane, (uint32_t)(2 * b + p_lane + i));
             x[i] = in ? *reinterpret_cast<const uint4 *>(b0 + at[i]) : make_uint4(kNegZero, kNegZero, kNegZero, kNegZero);
         }
-        op.template apply<Family, Grad>(L, o, k, row, o.n0 + cc, v, x, y0, y1);
+        op.template apply<Family, Grad>(L, o, k, row, o.n0 + cc, v, x, y0, y1, top);
         uint8_t *b1 = kTwo ? box(cb, 1) : nullptr;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -510,6 +525,11 @@ __device__ __noinline__ void finish_staged(const Op &op, const Geom &L, const Ti
             }
         }
     });
+    if constexpr (Grad)
+        if (op.top) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(op.largest(row, top)));
+            if (lane == 0) atomicMax(op.top, m);
+        }
     bulk_wait_all();  // the boxes have been read and written
 }
 
@@ -555,12 +575,6 @@ __device__ __forceinline__ void publish_sums(float4 *slice, uint32_t tq, int c, 
 
 // ---- kernel -------------------------------------------------------------------
 
-// Barrier of the decoder threads alone (the CTA's other warps do not take part).
-__device__ __forceinline__ void decoder_barrier(int threads)
-{
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-}
-
 template <class S, int BN, class Op, bool Pair>
 __global__ void __launch_bounds__(kWsThreadsOf<S>, 1)
 gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const __grid_constant__ Op op, int T,
@@ -572,7 +586,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     constexpr int kWsTileB = kBK * BN * 2 / (Pair ? 2 : 1);    // 32 or 64 KiB
     constexpr int kN = BN < 256 ? BN : 256;  // N of one MMA instruction
     constexpr int NG = kWsGroupsOf<S>;       // decoder groups
-    constexpr bool kTr = Op::kTransposed, kScaleW = Op::kScaleWeights;
+    constexpr bool kTr = Op::kTransposed;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -588,8 +602,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     uint64_t *in_bar = acc_full + 1;            // kStaged: the input's boxes, one per 64 tokens and lane quarter
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_bar + kInBoxes<Op, BN>);
     uint32_t *abort_flag = tmem_slot + 1;
-    uint32_t *scale_max = abort_flag + 1;       // kScaleW: largest |s| (binary16 bits)
-    uint32_t *last_flag = scale_max + 1;        // the last split of a tail tile
+    uint32_t *last_flag = abort_flag + 1;       // the last split of a tail tile
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int layer_stages = ws_layer_stages<Op>(L);
@@ -625,8 +638,8 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     // 1x16: codewords go from L2 into the tile by cp.async, as many stages in
     // flight as the ring holds (the copies arrive on the stage's barrier
     // themselves, and the MMA issuer orders them before its reads); other
-    // schemes, and weights that are scaled on the way, decode in registers
-    constexpr bool kAsyncWeights = (S::K == 1 && S::B == 16) && !kScaleW;
+    // schemes decode in registers
+    constexpr bool kAsyncWeights = S::K == 1 && S::B == 16;
     if (S::B == 16 && tid == 0) prefetch_table_share(op.w[0].cb, (uint32_t)S::K * 65536u * 16u);
     if constexpr (S::B == 16 && Op::kLayers > 1)
         if (tid == 32) prefetch_table_share(op.w[1].cb, (uint32_t)S::K * 65536u * 16u);
@@ -651,7 +664,6 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         mbar_init(acc_full, 1);
         for (int i = 0; i < kInBoxes<Op, BN>; ++i) mbar_init(&in_bar[i], 1);
         *abort_flag = 0;
-        *scale_max = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -820,31 +832,6 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         Chunk<S> code_ring[kCodeAhead];
 #pragma unroll
         for (int q = 0; q < kCodeAhead; ++q) code_ring[q] = fetch(dg + NG * q);
-        // kScaleW: the rows' scales, one per lane (rows of the warp's two
-        // row tiles), as far ahead as the codes; divided by 2^E where used
-        float inv = 1.f;
-        uint16_t scale_ring[kCodeAhead];
-        auto fetch_scale = [&](int s) -> uint16_t {
-            const int l = layer_of(s), o = (tile_of(s) - (rt_l & 1)) * 8 + (lane & 15);
-            if (s >= nk || o >= L.out) return (uint16_t)0;  // rows past the layer weigh nothing
-            const uint16_t *sc = op.w[l].scales;
-            return sc ? __ldg(sc + o) : (uint16_t)0x3c00;
-        };
-        if constexpr (kScaleW) {
-            grid_dependency_wait();  // the scales
-#pragma unroll
-            for (int q = 0; q < kCodeAhead; ++q) scale_ring[q] = fetch_scale(dg + NG * q);
-            uint32_t m = 0;
-            for (int l = 0; l < op.layers; ++l)
-                m = max(m, op.w[l].scales ? absmax_share(op.w[l].scales, L.out, tid - 64, 128 * NG) : 0x3c00u);
-            m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0) atomicMax(scale_max, m);
-            decoder_barrier(128 * NG);
-            m = *reinterpret_cast<volatile uint32_t *>(scale_max);
-            const int e = scale_exponent(m);
-            inv = ldexpf(1.f, -e);
-            out.factor = ldexpf(1.f, e);
-        }
         bool ok = true;
         // unrolled by the ring depth so every ring index is static
         for (int k0 = 0; ok && k0 < nown; k0 += kCodeAhead) {
@@ -857,7 +844,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     // the buffer is free once the MMAs of stage s - depth completed
                     if (s >= kWsAStages && !mbar_wait_ns(&empty_a[buf], ((s / kWsAStages) - 1) & 1, kWaitNs)) *abort_v = 1;
                     // a warp leaves together where its lanes act together
-                    if ((kScaleW || Pair) ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
+                    if (Pair ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
                         ok = false;
                         break;
                     }
@@ -866,40 +853,13 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     uint8_t *A = tileA + buf * kTileABytes;
                     const uint4 *books = scb + (Op::kLayers > 1 ? layer_of(s) * S::K * 256 : 0);
                     const uint4 *cb = op.w[Op::kLayers > 1 ? layer_of(s) : 0].cb;
-                    if constexpr (kScaleW) {
-                        const uint32_t mine = float_to_half_bits(half_bits_to_float(scale_ring[u]) * inv);
-                        auto put = [&](int r, uint4 v) {
-                            const uint32_t h = __shfl_sync(0xffffffffu, mine, (rt_l & 1) * 8 + r);
-                            const __half2 h2 = __half2half2(__ushort_as_half((uint16_t)h));
-                            uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __half2 m = __hmul2(*reinterpret_cast<__half2 *>(&p[j]), h2);
-                                // a row past the layer: zero, whatever its padding code selects
-                                p[j] = (live && tile_of(s) * 8 + r < L.out) ? *reinterpret_cast<const uint32_t *>(&m) : 0u;
-                            }
-                            *reinterpret_cast<uint4 *>(A + slot_of(r)) = make_uint4(p[0], p[1], p[2], p[3]);
-                        };
-                        if constexpr (S::K <= 2) {
-                            uint4 tt[8][S::K];
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) gather_terms<S>(code, r, books, cb, tt[r]);
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) put(r, sum_round_fast_h8<S::K>(tt[r]));
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                uint4 tt[S::K];
-                                gather_terms<S>(code, r, books, cb, tt);
-                                put(r, sum_round_fast_h8<S::K>(tt));
-                            }
-                        }
-                    } else if constexpr (kAsyncWeights) {
+                    // kTr: a row past the layer is zero, whatever its padding code selects
+                    auto real = [&](int r) { return live && (!kTr || tile_of(s) * 8 + r < L.out); };
+                    if constexpr (kAsyncWeights) {
                         const uint32_t a0 = smem_u32(A);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
-                            // kTr: a row past the layer is zero, whatever its padding code selects
-                            const bool in = live && (!kTr || tile_of(s) * 8 + r < L.out);
+                            const bool in = real(r);
                             cp_async16(a0 + slot_of(r), in ? (const void *)(cb + code.code(r, 0)) : (const void *)cb,
                                        in ? 16u : 0u);
                         }
@@ -912,14 +872,14 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             *reinterpret_cast<uint4 *>(A + slot_of(r)) =
-                                live ? sum_round_fast_h8<S::K>(tt[r]) : make_uint4(0, 0, 0, 0);
+                                real(r) ? sum_round_fast_h8<S::K>(tt[r]) : make_uint4(0, 0, 0, 0);
                     } else {
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
                             uint4 tt[S::K];
                             gather_terms<S>(code, r, books, cb, tt);
                             *reinterpret_cast<uint4 *>(A + slot_of(r)) =
-                                live ? sum_round_fast_h8<S::K>(tt) : make_uint4(0, 0, 0, 0);
+                                real(r) ? sum_round_fast_h8<S::K>(tt) : make_uint4(0, 0, 0, 0);
                         }
                     }
                 }
@@ -927,7 +887,6 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                 else publish(s);
                 // the next requests follow the fence, which would wait for them
                 code_ring[u] = fetch(s + NG * kCodeAhead);
-                if constexpr (kScaleW) scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
             }
         }
         cp_async_wait<0>();
@@ -947,8 +906,11 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             for (int s = max(0, nk - kWsStages); s < nk; ++s)
                 mbar_wait_ns(&full_b[s % kWsStages], (s / kWsStages) & 1, kWaitNs);
     }
-    if constexpr (kTr && !kScaleW)
-        if (op.factor) out.factor = __ldcg(op.factor);
+    if constexpr (kTr)
+        if (op.factor) {
+            out.factor = __ldcg(op.factor);
+            if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *op.top = 0u;
+        }
     // The decoder warps finish: warp & 3 is the TMEM lane quarter, the NG
     // warps of a quarter take alternate blocks of 64 columns (PlainOp: 16).
     // After a timeout no tensor memory is read and the output is incomplete,

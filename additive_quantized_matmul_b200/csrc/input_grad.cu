@@ -1,56 +1,37 @@
 // Input gradient of a quantised layer, gx = W^T (s gy), and of the gated
 // block's two layers at once: the transposed product on the warp-specialised
-// kernel of gemm_ws.cuh (BackOp).
+// kernel of gemm_ws.cuh (BackOp), which takes s gy (gemm_fused.cu).
 //
 // A CTA takes 128 input features and 256 or 512 tokens and walks the layer's
 // rows, 64 a stage: the codewords of 8 rows x 16 groups are laid along M
 // (MN-major A), gy rows come by TMA.  Two layers follow one another in the
-// same accumulator.  4096 x 4096 1x16, 512 tokens: 35 us in series, of which
-// the scaling of gy takes 5, the main loop 14 (32 tiles, the layer's rows split
-// over clusters of four) and the joined finish 11; 11008 x 4096 2x8, 2047
-// tokens: 206 us (896 TFLOP/s), 171 alone.
+// same accumulator.
 #include "gemm_ws.cuh"
 #include "layer_ops.cuh"
 
 namespace aqh {
 using namespace aqk;
 
-using AnyBack = BackOp<true>;  // both forms have the same plan
-
 static GemmPlan plan_back(const Geom &g, int layers, int T)
 {
-    return plan_ws(ws_mtiles<AnyBack>(g), layers * ws_layer_stages<AnyBack>(g), T, ws_max_bn<AnyBack>(g), AnyBack::kPairs);
+    return plan_ws(ws_mtiles<BackOp>(g), layers * ws_layer_stages<BackOp>(g), T, ws_max_bn<BackOp>(g), BackOp::kPairs);
 }
 
 size_t back_plan_bytes(const Geom &g, int layers, int T) { return plan_back(g, layers, T).ws_bytes; }
 
-template <bool Scaled>
-static cudaError_t launch(const Geom &g, int layers, const LayerWeights &w0, const uint16_t *g0, const LayerWeights &w1,
-                          const uint16_t *g1, int T, const float *factor, uint16_t *gx, void *ws, cudaStream_t s)
+cudaError_t launch_back(const Geom &g, int layers, const LayerWeights &w0, const uint16_t *g0, const LayerWeights &w1,
+                        const uint16_t *g1, int T, const float *factor, uint16_t *gx, void *ws, cudaStream_t s)
 {
-    using Op = BackOp<Scaled>;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
-    TensorMaps<Op::kMaps> maps{};
-    const Op op{{w0, layers > 1 ? w1 : w0}, layers, gx, factor};
+    TensorMaps<BackOp::kMaps> maps{};
+    const BackOp op{{w0, layers > 1 ? w1 : w0}, layers, gx, factor, ws_top(ws)};
     const int pitch = padded_tokens(T);
     if (!token_map(encode, &maps.m[0], g0, g.out, T, pitch) ||
         !token_map(encode, &maps.m[1], layers > 1 ? g1 : g0, g.out, T, pitch) ||
         !io_maps(encode, &maps, op, g, T, pitch))
         return cudaErrorInvalidValue;
-    const GemmPlan p = plan_back(g, layers, T);
-    return with_scheme(g, [&](auto sch) {
-        using S = decltype(sch);
-        if constexpr ((S::K == 1 && S::B == 16) != Scaled) return cudaErrorInvalidValue;  // see back_takes_scaled
-        else return launch_ws_scheme<S>(g, p, maps, op, T, ws, s, true);
-    });
-}
-
-cudaError_t launch_back(const Geom &g, int layers, const LayerWeights &w0, const uint16_t *g0, const LayerWeights &w1,
-                        const uint16_t *g1, int T, const float *factor, uint16_t *gx, void *ws, cudaStream_t s)
-{
-    return back_takes_scaled(g) ? launch<true>(g, layers, w0, g0, w1, g1, T, factor, gx, ws, s)
-                                : launch<false>(g, layers, w0, g0, w1, g1, T, nullptr, gx, ws, s);
+    return launch_ws(g, plan_back(g, layers, T), maps, op, T, ws, s, true);
 }
 
 }  // namespace aqh

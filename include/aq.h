@@ -110,7 +110,8 @@ size_t aq_packed_codes_bytes(const aq_layer_desc *desc);
  * Workspace.  aq_gemv, aq_gemm, aq_param_grad, aq_encode and the layer
  * operators further down take a caller-owned device workspace.  Its first 16 bytes hold a status word that
  * a kernel sets when a bounded wait gives up (read it with
- * aq_workspace_status); then come split-K arrival counters in a fixed area
+ * aq_workspace_status) and a word that the backward passes use between their
+ * launches; then come split-K arrival counters in a fixed area
  * of 4 KiB, then the call's own data (split-K partial sums, tables).  A
  * workspace must be zero-filled once before its first use; every completed
  * call leaves it ready for the next (counters back at zero), whatever the
@@ -405,12 +406,12 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  * y = diag(s) W x,
  *   gx[i][t] = RN16(sum_o W[o][i] s[o] gy[o][t]),   gy [out][T], gx [in][T],
  * 1 <= T <= 2^22.  The tensor cores take binary16 operands, so s is multiplied
- * into one of them, divided by 2^E, the power of two just above the largest
- * |s| (nothing overflows, and uniformly small scales lose no bits): into the
- * weights, or for 1x16 layers into gy.  That operand carries one rounding of at
- * most 2^-11 of its value plus 2^-25; 2^E is applied to the fp32 sum.  gx
- * overlaps no input.  Together with aq_param_grad this is the backward pass of
- * aq_gemm.  Deterministic; the workspace holds
+ * into gy: s gy / 2^E is rounded once and 2^E applied to the fp32 sum.  2^E brings
+ * the largest finite |s gy| of the call to 2^14 .. 2^15, so that nothing
+ * overflows and gradients and scales of any size keep their bits: the rounding
+ * is at most 2^-11 of the product plus 2^-39 of the largest one.  (Without scales
+ * gy is taken as it is.)  gx overlaps no input.  Together with aq_param_grad
+ * this is the backward pass of aq_gemm.  Deterministic; the workspace holds
  * aq_input_grad_workspace_bytes(desc, T) bytes.
  */
 size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T);
@@ -461,7 +462,7 @@ aq_status aq_glu_gemm(const aq_layer_desc *desc, const aq_weights *gate, const a
  *   grad_gate = RN16(gy u act'(g)),  grad_up = RN16(gy act(g))     [out][T]
  *   grad_x    = RN16(W_g^T (s_g grad_gate) + W_u^T (s_u grad_up))  [in][T], NULL to skip
  * (of the rounded grad_gate and grad_up; the transposed products as in
- * aq_input_grad, with one E for both layers).  aq_param_grad(x, grad_gate)
+ * aq_input_grad, one E for both layers' products).  aq_param_grad(x, grad_gate)
  * and (x, grad_up) give the scales' and codebooks' gradients.  1 <= T <=
  * 2^22.  Deterministic.  The outputs overlap no input and not
  * one another.

@@ -12,7 +12,7 @@ from test_gpu_layer_ops import Case, acts, fenced, half
 
 pytestmark = pytest.mark.gpu
 
-COUNTERS = slice(16, 16 + 4 * 1024)
+HEAD = slice(0, 16 + 4 * 1024)  # status word, largest scaled gradient, arrival counters
 
 
 class Block:
@@ -90,7 +90,7 @@ class Block:
                                              (11008, 4096, 1, 16), (1000, 1032, 333, 2)])
 def test_one_workspace_for_any_sequence_of_calls(K, B, out, inp, T, batch):
     """Every call, on a workspace that every other call used before it, gives
-    the bits it gives on a workspace of its own, and leaves the arrival
+    the bits it gives on a workspace of its own, and leaves status word and
     counters at zero."""
     calls = Block(out, inp, K, B, 5).calls(T, batch)
     alone = {}
@@ -104,7 +104,7 @@ def test_one_workspace_for_any_sequence_of_calls(K, B, out, inp, T, batch):
     for name, _, go in order:
         got = go(shared)
         torch.cuda.synchronize()
-        assert int(shared[COUNTERS].max()) == 0, f"{name} left a counter"
+        assert int(shared[HEAD].max()) == 0, f"{name} left something in the head"
         for i, (a, b) in enumerate(zip(got, alone[name])):
             a = a.view(torch.int16) if a.dtype == torch.float16 else a
             assert torch.equal(a, b), f"{name} output {i}"
@@ -133,7 +133,7 @@ def test_training_step_twice_on_one_workspace(K, B, T):
         aq.aq_glu_grad(ff.desc, *ff.weights, xd, gh[1], T, 4, gg[1], gu[1], gx[1], ws)
         aq.aq_gemm(*down.w(), h[1], T, z[1], ws)
     torch.cuda.synchronize()
-    assert aq.aq_workspace_status(ws) == 0 and int(ws[COUNTERS].max()) == 0
+    assert aq.aq_workspace_status(ws) == 0 and int(ws[HEAD].max()) == 0
     assert all(guards_intact(b[0]) for b in (h, y, z, gh, gg, gu, gx))
     H, GH, GG, GU = (half(b[1], 520, T) for b in (h, gh, gg, gu))
     lr.check(H, lr.glu(*ff.refs, x, "silu"), "h")
@@ -277,3 +277,103 @@ def test_table_entries_of_small_activations_keep_their_bits(K, B, sigma):
     for got, want, var in ((c.fused(x, "none"), zg, vg), (c.glu(x, "none"), zg * zu, zu ** 2 * vg + zg ** 2 * vu)):
         err = got[:, 0].astype(np.float64) - want
         assert np.sqrt((err ** 2).mean()) <= 1.2 * np.sqrt((var + _step2(want)).mean())
+
+
+def _back(pairs):
+    """sum of W^T (s g) over [(Ref, g)], and its mean square error when each
+    product s g is rounded once to 11 bits and so is the result."""
+    total = var = 0.0
+    for r, g in pairs:
+        z = r.s[:, None] * lr.f64(g)
+        steps = np.where(z == 0, 0.0, 4.0 ** (np.floor(np.log2(np.abs(z) + (z == 0))) - 10) / 12)
+        total = total + r.W.T @ z
+        var = var + (r.W ** 2).T @ steps
+    return total, var + _step2(total)
+
+
+def _check_rms(got, pairs, what):
+    """The root mean square error over all elements; 1.2 leaves room for the
+    estimate's spread (thousands of rounding errors) and the fp32 sums."""
+    want, var = _back(pairs)
+    err = got.astype(np.float64) - want
+    assert np.isfinite(err).all(), what
+    ratio = np.sqrt((err ** 2).mean() / var.mean())
+    assert ratio <= 1.2, f"{what}: {ratio:.3g} times the error of one rounding"
+
+
+SCHEMES = [(1, 16), (2, 8), (1, 8), (2, 16), (8, 8)]
+
+
+@pytest.mark.parametrize("K,B", SCHEMES)
+@pytest.mark.parametrize("T", [3, 40, 45, 520])
+@pytest.mark.parametrize("sigma,scale", [(0.1, 1.0), (1e-3, 16.0), (1e-5, 1000.0), (1e-6, 10000.0), (100.0, 1e-3)])
+def test_gradients_of_any_size_keep_their_bits(K, B, T, sigma, scale):
+    """Small gradients times ordinary or large scales (and the other way round)
+    are rounded to 11 bits as the rest are."""
+    c = Case(520, 264, K, B, 34, scale=scale)
+    gy = acts(520, T, 4, sigma)
+    _check_rms(c.input_grad(gy), [(c.refs[0], gy)], "input grad")
+
+
+@pytest.mark.parametrize("K,B", SCHEMES)
+@pytest.mark.parametrize("T", [40, 45])
+def test_a_dominating_scale_costs_the_other_rows_no_bits(K, B, T):
+    c = Case(520, 264, K, B, 35)
+    s = (c.refs[0].s * 2.0 ** -11).astype(np.float16)
+    s[17] = np.float16(1024.0)
+    c.scales[0] = fenced(s)
+    c.refs[0].s = s.astype(np.float64)
+    gy = acts(520, T, 4, 64.0)
+    gy[17] = 0
+    _check_rms(c.input_grad(gy), [(c.refs[0], gy)], "input grad")
+
+
+@pytest.mark.parametrize("K,B", SCHEMES)
+@pytest.mark.parametrize("T", [8, 45, 520])
+@pytest.mark.parametrize("small", [0, 1])
+@pytest.mark.parametrize("power", [10, 12, 14])
+def test_gated_backward_of_layers_with_scales_of_different_size(K, B, T, small, power):
+    """One projection's scales 2^-power of the other's: the two terms of grad_x
+    are of one size (each layer's gradient carries the other's scale), so both
+    keep their bits."""
+    c = Case(520, 264, K, B, 36, layers=2)
+    s = (c.refs[small].s * 2.0 ** -power).astype(np.float16)
+    c.refs[small].s = s.astype(np.float64)
+    c.scales[small] = fenced(s)
+    c.weights = [aq.Weights.make(d.packed, b, k) for d, b, k in zip(c.dls, c.books, c.scales)]
+    x, gy = acts(264, T, 1), acts(520, T, 2, 30.0)
+    gg, gu, gx = c.glu_grad(x, gy, "silu")
+    want_g, want_u = lr.glu_grad(*c.refs, x, gy, "silu")
+    lr.check(gg, want_g, "grad_gate")
+    lr.check(gu, want_u, "grad_up")
+    _check_rms(gx, [(c.refs[0], gg), (c.refs[1], gu)], "grad_x")
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("T", [24, 45])
+def test_infinite_and_nan_gradients_stay_in_their_tokens(K, B, T):
+    """E follows the finite products: the other tokens keep their values' bits
+    but for the power of two."""
+    c = Case(520, 264, K, B, 37)
+    gy = acts(520, T, 4, 0.1)
+    bad = gy.copy()
+    bad[3, 2] = np.float16(np.inf)
+    bad[400, T - 1] = np.float16(np.nan)
+    clean, got = c.input_grad(gy), c.input_grad(bad)
+    keep = np.setdiff1d(np.arange(T), [2, T - 1])
+    lr.check(got[:, keep], tuple(a[:, keep] for a in c.refs[0].back(gy)), "other tokens")
+    assert np.isfinite(clean.astype(np.float64)).all()
+    assert _same_kind(got[:, 2], c.refs[0].W[3] * np.inf) and np.isnan(got[:, T - 1].astype(np.float64)).all()
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("T", [8, 13])
+@pytest.mark.parametrize("zero", ["gradients", "scales"])
+def test_zero_gradients_or_scales_give_zero(K, B, T, zero):
+    c = Case(136, 264, K, B, 38)
+    gy = acts(136, T, 4)
+    if zero == "gradients":
+        gy[...] = 0
+    else:
+        c.scales[0] = fenced(np.zeros(136, np.float16))
+    assert (c.input_grad(gy) == 0).all()
