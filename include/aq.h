@@ -33,13 +33,15 @@
  *    library (described at that function);
  *  - work is enqueued on `stream` (NULL = legacy default stream) and the
  *    call returns after the launch; the caller synchronises;
- *  - the GEMV kernels use programmatic dependent launch: a GEMV may start
- *    reading its weights (packed codes, codebooks) while the GEMV launched
- *    just before it on the stream is still running; it reads x and writes
- *    y and the workspace only after that launch has completed.  GEMVs write
- *    no weights, and other kernels (this library's or the caller's) let the
- *    next launch start only when they complete, so stream order holds for
- *    every value a caller can observe;
+ *  - the products (aq_gemv, aq_gemm and the layer operators) use programmatic
+ *    dependent launch: a product may start reading its weights (packed codes,
+ *    codebooks) while products launched before it on the stream are still
+ *    running; it reads everything else, and writes, only after they have
+ *    completed.  Products write no weights, and a kernel that does not let its
+ *    dependents start early (aq_pack_codes, aq_encode, aq_param_grad, any
+ *    ordinary kernel or copy of the caller) holds the next launch back until
+ *    it completes, so stream order holds for every value a caller can observe,
+ *    but for the two cases named under "Early weight reads" at aq_gemv;
  *  - all arguments are validated on the host before anything is launched;
  *    on any error status nothing is launched and no output byte is written;
  *  - array pointers must be 16-byte aligned (AQ_ERR_MISALIGNED otherwise);
@@ -182,16 +184,21 @@ aq_status aq_dequant(const aq_layer_desc *desc, const void *packed, const uint16
  * Results are deterministic: the same inputs give the same bits.
  * AQ_ERR_INVALID_ARG for batch outside 1..16.
  * Early weight reads: this kernel is launched with programmatic dependent
- * launch and may read `packed` and `codebooks` before the kernel launched
- * just before it on `stream` has finished (x, scales, y and the workspace
- * only after).  That is safe whenever the previous kernel does not write
- * this layer's packed codes or codebooks, or does not let its dependents
- * start early (griddepcontrol.launch_dependents / cudaTriggerProgrammatic-
- * LaunchCompletion) -- every kernel of this library and every kernel that
- * does not use programmatic launch qualifies.  A caller whose own kernel
- * triggers its dependents early and then rewrites these weights (a
- * fine-tuning step, for instance) must write them before the trigger, or
- * call aq_gemv_ordered instead.
+ * launch and may read `packed` and `codebooks` while kernels launched before it
+ * on `stream` are still running that let their dependents start early
+ * (griddepcontrol.launch_dependents / cudaTriggerProgrammaticLaunchCompletion;
+ * the products of this library do, so that the kernel before such a product
+ * may still be running too).  x, scales, y and the workspace follow their
+ * completion.  Kernels that do not trigger early have completed, so weights
+ * that they wrote are read as written.  Two cases are left to the caller:
+ *  - a kernel of the caller's that triggers its dependents early and then
+ *    rewrites these weights (a fine-tuning step, for instance);
+ *  - the output of one of this library's products, or of
+ *    a layer operator, passed as `packed` or `codebooks` of a later call.
+ * There the weights must be written before the trigger, or the first call of
+ * this library after them be ordered: aq_gemv_ordered or aq_gemm_ordered, or any
+ * call of this header with work between it and the writer that does not trigger
+ * early -- an ordinary kernel, or a cudaMemsetAsync of a spare word on `stream`.
  */
 aq_status aq_gemv(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
                   const uint16_t *scales, const uint16_t *x, int batch, uint16_t *y,
@@ -260,10 +267,8 @@ aq_status aq_gemv_noalloc(const aq_layer_desc *desc, const void *packed, const u
  * aq_workspace_status), frees its tensor memory and returns; the output is
  * then incomplete but the context stays usable.
  * Early weight reads: for T a multiple of 8 the kernel is launched with
- * programmatic dependent launch, as aq_gemv is, and may read `packed` and
- * `codebooks` before the kernel launched just before it on `stream` has
- * finished (x, scales, y and the workspace only after); aq_gemv's rule on
- * early weight reads applies, and aq_gemm_ordered is the ordinary launch.
+ * programmatic dependent launch, and aq_gemv's rule on early weight reads
+ * applies; aq_gemm_ordered is the ordinary launch.
  */
 aq_status aq_gemm(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
                   const uint16_t *scales, const uint16_t *x, int T, uint16_t *y,
@@ -380,9 +385,10 @@ typedef struct {
  * aq_gemm_fused_workspace_bytes.  `ep` NULL means no bias, no activation, no
  * residual.  y may be the residual array itself (each element is read before
  * it is written, by the thread that writes it) but overlaps no other input.
- * Other arguments, determinism, programmatic launch and early weight reads
- * as for aq_gemv and aq_gemm; bias and residual are read only after the
- * previous work on the stream.  AQ_ERR_INVALID_ARG for an unknown
+ * Other arguments and determinism as for aq_gemv and aq_gemm; bias and residual
+ * are read only after the previous work on the stream.  Early weight reads:
+ * aq_gemv's rule applies (ordinary work between, where it asks for order: there
+ * are no ordered forms).  AQ_ERR_INVALID_ARG for an unknown
  * activation or y = x; AQ_ERR_MISALIGNED for a residual off a 16-byte or a
  * bias off a 2-byte boundary.
  * With one or two 8-bit codebooks at batch 1 the products come from lookup
@@ -412,7 +418,8 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  * is at most 2^-11 of the product plus 2^-39 of the largest one.  (Without scales
  * gy is taken as it is.)  gx overlaps no input.  Together with aq_param_grad
  * this is the backward pass of aq_gemm.  Deterministic; the workspace holds
- * aq_input_grad_workspace_bytes(desc, T) bytes.
+ * aq_input_grad_workspace_bytes(desc, T) bytes.  Early weight reads: aq_gemv's
+ * rule applies, as for aq_gemm_fused.
  */
 size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T);
 aq_status aq_input_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
@@ -429,7 +436,8 @@ aq_status aq_input_grad(const aq_layer_desc *desc, const void *packed, const uin
  * gradient is gy itself; aq_param_grad(x, grad_z) gives the scales' and
  * codebooks'.  ep->residual is ignored.  The sums of grad_bias take a fixed
  * order: deterministic.  1 <= T <= 2^22.  The outputs overlap no input and
- * not one another.
+ * not one another.  Early weight reads: aq_gemv's rule applies, as for
+ * aq_gemm_fused.
  */
 size_t aq_gemm_fused_grad_workspace_bytes(const aq_layer_desc *desc, int T);
 aq_status aq_gemm_fused_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
@@ -443,9 +451,9 @@ aq_status aq_gemm_fused_grad(const aq_layer_desc *desc, const void *packed, cons
  * for two layers of the same descriptor.  aq_glu_gemv takes batch 1..16 and
  * out <= 131072 (its two projections meet at one arrival counter per 128
  * rows; AQ_ERR_INVALID_ARG above), aq_glu_gemm 1 <= T <= 2^22 tokens.
- * `activation` is an aq_activation, applied to the gate.  y overlaps no input.  Launch,
- * early weight reads (of both layers) and determinism as for aq_gemv and
- * aq_gemm.
+ * `activation` is an aq_activation, applied to the gate.  y overlaps no input.
+ * Determinism as for aq_gemv and aq_gemm.  Early weight reads, of both layers:
+ * aq_gemv's rule applies, as for aq_gemm_fused.
  */
 size_t aq_glu_gemv_workspace_bytes(const aq_layer_desc *desc, int batch);
 size_t aq_glu_gemm_workspace_bytes(const aq_layer_desc *desc, int T);
@@ -465,7 +473,8 @@ aq_status aq_glu_gemm(const aq_layer_desc *desc, const aq_weights *gate, const a
  * aq_input_grad, one E for both layers' products).  aq_param_grad(x, grad_gate)
  * and (x, grad_up) give the scales' and codebooks' gradients.  1 <= T <=
  * 2^22.  Deterministic.  The outputs overlap no input and not
- * one another.
+ * one another.  Early weight reads, of both layers: aq_gemv's rule applies, as
+ * for aq_gemm_fused.
  */
 size_t aq_glu_grad_workspace_bytes(const aq_layer_desc *desc, int T);
 aq_status aq_glu_grad(const aq_layer_desc *desc, const aq_weights *gate, const aq_weights *up, const uint16_t *x,

@@ -377,3 +377,39 @@ def test_zero_gradients_or_scales_give_zero(K, B, T, zero):
     else:
         c.scales[0] = fenced(np.zeros(136, np.float16))
     assert (c.input_grad(gy) == 0).all()
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("T,batch", [(48, 1), (45, 2), (520, 8)])
+def test_weights_rewritten_by_ordinary_work_between_calls(K, B, T, batch):
+    """Every entry point right behind another call and a copy that rewrites the
+    codebooks (as an optimiser step would), all queued at once: each call sees the
+    codebooks that the last copy left."""
+    b = Block(1000, 1032, K, B, 9)
+    calls = b.calls(T, batch)
+    sets = [[books.clone() for _, books, _ in b.w],
+            [(torch.randn(books.shape, device="cuda", generator=b.gen) * 0.02).half() for _, books, _ in b.w]]
+
+    def write(i):
+        for (_, books, _), new in zip(b.w, sets[i]):
+            books.copy_(new)
+
+    ws = workspace(max(size for _, size, _ in calls))
+    want = []
+    for i in (0, 1):
+        write(i)
+        torch.cuda.synchronize()
+        want.append([[o.clone() for o in go(ws)] for _, _, go in calls])
+        torch.cuda.synchronize()
+    got = []
+    for j in range(len(calls)):
+        for i in (0, 1, 0):
+            write(i)
+            got.append((j, i, calls[j][2](ws), calls[j - 1][2](ws)))
+    torch.cuda.synchronize()
+    assert aq.aq_workspace_status(ws) == 0
+    for j, i, outs, before in got:
+        for k, o in ((j, outs), (j - 1, before)):
+            for x, y in zip(o, want[i][k]):
+                x, y = (t.view(torch.int16) if t.dtype == torch.float16 else t for t in (x, y))
+                assert torch.equal(x, y), (calls[k][0], i)

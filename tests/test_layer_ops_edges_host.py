@@ -1,5 +1,8 @@
 """Layer operators at their edges, without a GPU: what the sizes and the header
 promise."""
+import os
+import re
+
 import pytest
 
 import additive_quantized_matmul_b200 as aq
@@ -30,3 +33,30 @@ def test_arrays_lie_behind_the_counters(K, B, out, inp, T):
                        (aq.aq_glu_grad_workspace_bytes, 2 * pad_in + 3 * pad_out + 2 * scaled)):
         if arrays:
             assert fn(d, T) >= DATA + arrays, fn.__name__
+
+
+# entry points whose first launch may read weights before earlier launches complete
+EARLY = ["aq_gemv", "aq_gemv_noalloc", "aq_gemm", "aq_gemv_fused", "aq_gemm_fused", "aq_input_grad",
+         "aq_gemm_fused_grad", "aq_glu_gemv", "aq_glu_gemm", "aq_glu_grad"]
+
+
+def _header():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "aq.h")
+    with open(path, encoding="utf-8") as f:
+        return f.read()
+
+
+@pytest.mark.parametrize("fn", EARLY)
+def test_the_header_names_the_rule_where_weights_are_read_early(fn):
+    text = _header()
+    at = text.index(f"aq_status {fn}(")
+    comment = text[text.rindex("/*", 0, at):at]
+    assert "early weight reads" in " ".join(comment.replace("*", " ").split()).lower()
+
+
+def test_every_function_that_the_header_speaks_of_exists():
+    text = _header()
+    declared = set(re.findall(r"\b(aq_\w+)\(", text)) | set(re.findall(r"}\s*(aq_\w+);", text)) | {"aq_b200", "aq_stream_t"}
+    spoken = set(re.findall(r"\b(aq_[a-z0-9_]+)\b", text))
+    assert spoken <= declared, spoken - declared
+    assert set(aq.EXPORTED_SYMBOLS) <= declared
