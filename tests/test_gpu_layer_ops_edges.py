@@ -413,3 +413,20 @@ def test_weights_rewritten_by_ordinary_work_between_calls(K, B, T, batch):
             for x, y in zip(o, want[i][k]):
                 x, y = (t.view(torch.int16) if t.dtype == torch.float16 else t for t in (x, y))
                 assert torch.equal(x, y), (calls[k][0], i)
+
+
+@pytest.mark.parametrize("K,B", [(1, 16), (2, 8)])
+@pytest.mark.parametrize("out,T", [(8, 5001), (24, 2056), (520, 4099)])
+def test_the_largest_gradient_is_found_wherever_it_stands(K, B, out, T):
+    """Gradients of 1e-3 and one of 6e4, in the first or last rows and tokens,
+    the ends of a warp's share of a row (2048 tokens) among them: a largest one
+    that was missed would overflow once scaled."""
+    c = Case(out, 136, K, B, 39, sigma=1e-3)
+    base = acts(out, T, 4, 1e-3)
+    for r, t in ((0, 0), (out - 1, T - 1), (out // 2, 2047), (out - 1, 2048), (0, T - 2)):
+        gy = base.copy()
+        gy[r, t] = np.float16(6e4)
+        got = c.input_grad(gy)
+        toks = np.unique([0, 7, 8, 2046, 2047, 2048, 2049, T - 9, T - 2, T - 1, t])
+        lr.check(got[:, toks], c.refs[0].back(gy[:, toks]), f"row {r} token {t}")
+        assert np.isfinite(got.astype(np.float64)).all()
