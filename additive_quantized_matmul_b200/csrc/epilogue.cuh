@@ -134,6 +134,37 @@ __device__ __forceinline__ float scaled_top(uint32_t m, float s)
     return fabsf(s) < 65536.f ? fabsf(s) * fmaxf(f.x, f.y) : 0.f;
 }
 
+// Largest finite |v| (as the bits of a binary16) of this thread's share of
+// v[0 .. n), `threads` threads in all.
+__device__ __forceinline__ uint32_t finite_absmax_share(const uint16_t *__restrict__ v, int n, int thread, int threads)
+{
+    uint32_t m = 0;
+    // 16-byte pieces between the ragged ends (v has 2-byte alignment)
+    const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(v) & 15)) & 15) / 2);
+    const int nv = (n - head) / 8;
+    const uint4 *v4 = reinterpret_cast<const uint4 *>(v + head);
+#pragma unroll 8
+    for (int i = thread; i < nv; i += threads) finite_absmax_h8(m, __ldg(v4 + i));
+    if (thread < head) finite_absmax_h2(m, v[thread]);
+    if (head + nv * 8 + thread < n && thread < 8) finite_absmax_h2(m, v[head + nv * 8 + thread]);
+    return max(m & 0xffffu, m >> 16);
+}
+
+// The transposed product of layers with one or two 8-bit codebooks multiplies the
+// scales into the weights, divided by 2^E: of the largest scale (bits `s`) and the
+// largest entry of a codebook (bits `c`), E is the smallest for which no |W s| / 2^E
+// reaches 2^15 (|W| <= K c, but for infinite weights; with c of 2^14 and more, none
+// reaches 65504), nor any s / 2^E.  What is subnormal then, a scale or a weight
+// times a scale, is less than 2^-14 2^E; with codebook entries up to 1/2 or 1/4
+// that is 2^-29 of the largest scale.
+__device__ __forceinline__ int weight_exponent(uint32_t s, uint32_t c, int K)
+{
+    if (s == 0) return 0;
+    const int es = ilogbf(half_bits_to_float((uint16_t)s)) + 1;
+    const int ec = c ? ilogbf((float)K * half_bits_to_float((uint16_t)c)) + 1 : 0;
+    return es - max(0, 15 - max(ec, 0));
+}
+
 // One layer's stored weights on the device.
 struct LayerWeights {
     const uint8_t *packed;

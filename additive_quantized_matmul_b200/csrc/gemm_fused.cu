@@ -391,17 +391,23 @@ void take_padded(Layout &l, const Geom &g, int T, int in_arrays, int out_arrays)
     for (int i = 0; i < out_arrays; ++i) l.take(padded_bytes(g.out, T));
 }
 
-// The gradients that the transposed product reads: as they are, or, of layers
-// with scales, copies multiplied by them.
+// The gradients that the transposed product reads: as they are, or copies
+// multiplied by the layers' scales.
 struct Scaled {
     const uint16_t *g[2];
-    const float *factor;  // or null
+    float *factor;  // or null
 };
 
 void take_scaled(Layout &l, const Geom &g, int T, int layers)
 {
+    if (back_scales_weights(g)) return;
     l.take(sizeof(float));
     for (int i = 0; i < layers; ++i) l.take(padded_bytes(g.out, T));
+}
+
+bool scaled_gradients(const Geom &g, const LayerWeights &w0, const LayerWeights &w1)
+{
+    return !back_scales_weights(g) && (w0.scales || w1.scales);
 }
 
 // `pitch`: of the gradients in memory (T where they are ragged and unpadded);
@@ -410,9 +416,9 @@ cudaError_t scale_gradients(const Geom &g, Layout &l, char *ws, int layers, cons
                             const uint16_t *const *grads, int T, int pitch, bool known, Scaled *out, cudaStream_t s)
 {
     *out = Scaled{{grads[0], layers > 1 ? grads[1] : grads[0]}, nullptr};
-    const bool scales = w[0].scales || (layers > 1 && w[1].scales);
+    const bool scales = scaled_gradients(g, w[0], layers > 1 ? w[1] : w[0]);
     if (!scales && pitch == padded_tokens(T)) return cudaSuccess;
-    float *factor = reinterpret_cast<float *>(ws + l.take(sizeof(float)));
+    if (scales) out->factor = reinterpret_cast<float *>(ws + l.take(sizeof(float)));
     RowCopy jobs[2];
     for (int i = 0; i < layers; ++i) {
         uint16_t *z = reinterpret_cast<uint16_t *>(ws + l.take(padded_bytes(g.out, T)));
@@ -420,8 +426,7 @@ cudaError_t scale_gradients(const Geom &g, Layout &l, char *ws, int layers, cons
         out->g[i] = z;
     }
     if (!scales) return copy_rows(jobs, layers, T, s);
-    out->factor = factor;
-    return scale_rows(jobs, layers, T, factor, ws_top(ws), known, s);
+    return scale_rows(jobs, layers, T, out->factor, ws_top(ws), known, s);
 }
 
 size_t bias_sums_bytes(const Geom &g, int T) { return (size_t)((T + 15) / 16) * g.out * sizeof(float); }
@@ -493,7 +498,7 @@ cudaError_t launch_gemm_fused_grad(const Geom &g, const LayerWeights &w, const u
     const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
     uint16_t *zk = a.out(grad_z, g.out), *gxk = a.out(grad_x, g.in);
     const FusedOp op{{w}, ep.act, ep.bias, gk, zk, true, grad_bias ? sums : nullptr,
-                     grad_x && w.scales ? ws_top(ws) : nullptr};
+                     grad_x && scaled_gradients(g, w, w) ? ws_top(ws) : nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     if (e == cudaSuccess && grad_bias)
@@ -524,7 +529,7 @@ cudaError_t launch_glu_grad(const Geom &g, const LayerWeights &gate, const Layer
     Arrays a(l, base, T);
     const uint16_t *xk = a.in(x, g.in), *gk = a.in(gy, g.out);
     uint16_t *ggk = a.out(grad_gate, g.out), *guk = a.out(grad_up, g.out), *gxk = a.out(grad_x, g.in);
-    const GatedOp op{{gate, up}, act, gk, ggk, guk, grad_x && (gate.scales || up.scales) ? ws_top(ws) : nullptr};
+    const GatedOp op{{gate, up}, act, gk, ggk, guk, grad_x && scaled_gradients(g, gate, up) ? ws_top(ws) : nullptr};
     cudaError_t e = a.before(s);
     if (e == cudaSuccess) e = product(g, l, xk, T, op, base, s);
     if (e == cudaSuccess && grad_x) {

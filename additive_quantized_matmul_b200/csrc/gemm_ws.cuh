@@ -49,9 +49,10 @@
 //    runs over the layer's rows (of one or two layers, one after the other):
 //    thread t decodes chunk (row tile t/16, group t%16) and its codewords
 //    lie along M, so A is MN-major like B.  The row scale belongs to the
-//    contraction index and is multiplied, divided by 2^E, into the other
-//    operand before (scale_rows in layer_ops.cuh: one rounding to binary16);
-//    2^E is applied to the fp32 sums.
+//    contraction index and is multiplied, divided by 2^E, into the weights (one
+//    or two 8-bit codebooks, weight_exponent) or, before, into the other operand
+//    (scale_rows in layer_ops.cuh): one rounding to binary16; 2^E is applied to
+//    the fp32 sums.
 #pragma once
 
 #include <cuda.h>
@@ -158,6 +159,7 @@ struct TileOut {
 // y = RN16(s (W x)); T % 8 == 0.
 struct PlainOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = false;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kMaps = 1, kXMaps = 1, kAhead = 4;
     static constexpr bool kPairs = false;
     LayerWeights w[1];
@@ -168,6 +170,7 @@ struct PlainOp {
 // act'(z)) and the sums of gy act'(z) over each block of 16 tokens.
 struct FusedOp {
     static constexpr bool kGated = false, kTransposed = false, kStaged = true;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 1, kXMaps = 1, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -226,7 +229,8 @@ struct FusedOp {
                 }
             }
             y0[h] = round_h8(a);
-            if constexpr (Grad) finite_absmax_h8(m[0], y0[h]);
+            if constexpr (Grad)
+                if (top) finite_absmax_h8(m[0], y0[h]);
         }
         if constexpr (Grad) {
             const int i = row0(o) + (int)(threadIdx.x & 31);
@@ -239,6 +243,7 @@ struct FusedOp {
 // Gated block: y = RN16(act(g) u), or, with gy, the gradients of g and u.
 struct GatedOp {
     static constexpr bool kGated = true, kTransposed = false, kStaged = true;
+    static constexpr bool kScaleWeights = false;
     static constexpr int kLayers = 2, kXMaps = 1, kRows = 16, kPieces = 1, kOutputs = 2, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
@@ -301,8 +306,10 @@ struct GatedOp {
         y0[0] = round_h8(a);
         if constexpr (Grad) {
             y1[0] = round_h8(c);
-            finite_absmax_h8(m[0], y0[0]);
-            finite_absmax_h8(m[1], y1[0]);
+            if (top) {
+                finite_absmax_h8(m[0], y0[0]);
+                finite_absmax_h8(m[1], y1[0]);
+            }
         }
     }
     __device__ __forceinline__ float largest(const Row &r, const uint32_t (&m)[2]) const
@@ -313,20 +320,25 @@ struct GatedOp {
     }
 };
 
-// gx = RN16(2^E sum over the layers of W^T g), g = s gy / 2^E: the scales are in
-// g, so that the weights go into shared memory as they are (1x16: by
-// asynchronous copies; scaling them on the way through registers took 2207
-// cycles a stage against 1400, and a weight times a scale far below the largest
-// one would be subnormal).
+// gx = RN16(2^E sum over the layers of W^T (s gy / 2^E)).  ScaleW: the decoders
+// scale the weights, which pass through registers anyway, with E from the largest
+// scale and codebook entry.  Else the scales are in gy, with E from the largest
+// product: 16-bit codebooks are too long to look through in a CTA, 1x16 weights go
+// into shared memory by asynchronous copies (scaling them on the way through
+// registers took 2207 cycles a stage against 1400), and 8x8 decoders have no time
+// to spare (input gradient 11008 x 4096, 2048 tokens 892 -> 856 us; 2x8, which
+// would need two passes over the gradients, 206 -> 175 with scaled weights).
+template <bool ScaleW>
 struct BackOp {
     static constexpr bool kGated = false, kTransposed = true, kStaged = true;
+    static constexpr bool kScaleWeights = ScaleW;
     static constexpr int kLayers = 2, kXMaps = 2, kRows = 32, kPieces = 2, kOutputs = 1, kAhead = 4;
     static constexpr int kMaps = kXMaps + 3;
     static constexpr bool kPairs = true;
     LayerWeights w[2];
     int layers;  // 1 or 2
     uint16_t *gx;
-    const float *factor;  // 2^E, or null: 1
+    const float *factor;  // !ScaleW: 2^E, or null: 1
     unsigned *top;        // with factor: to be cleared
     static constexpr int act = AQ_ACT_NONE;
 
@@ -575,6 +587,12 @@ __device__ __forceinline__ void publish_sums(float4 *slice, uint32_t tq, int c, 
 
 // ---- kernel -------------------------------------------------------------------
 
+// Barrier of the decoder threads alone (the CTA's other warps do not take part).
+__device__ __forceinline__ void decoder_barrier(int threads)
+{
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
 template <class S, int BN, class Op, bool Pair>
 __global__ void __launch_bounds__(kWsThreadsOf<S>, 1)
 gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const __grid_constant__ Op op, int T,
@@ -586,7 +604,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     constexpr int kWsTileB = kBK * BN * 2 / (Pair ? 2 : 1);    // 32 or 64 KiB
     constexpr int kN = BN < 256 ? BN : 256;  // N of one MMA instruction
     constexpr int NG = kWsGroupsOf<S>;       // decoder groups
-    constexpr bool kTr = Op::kTransposed;
+    constexpr bool kTr = Op::kTransposed, kScaleW = Op::kScaleWeights;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -603,6 +621,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(in_bar + kInBoxes<Op, BN>);
     uint32_t *abort_flag = tmem_slot + 1;
     uint32_t *last_flag = abort_flag + 1;       // the last split of a tail tile
+    uint32_t *scale_max = last_flag + 1;        // kScaleW: largest |s| and |C| (binary16 bits)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int layer_stages = ws_layer_stages<Op>(L);
@@ -640,6 +659,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
     // themselves, and the MMA issuer orders them before its reads); other
     // schemes decode in registers
     constexpr bool kAsyncWeights = S::K == 1 && S::B == 16;
+    static_assert(!kScaleW || (S::kBooksInSmem && S::K <= 2), "see BackOp");
     if (S::B == 16 && tid == 0) prefetch_table_share(op.w[0].cb, (uint32_t)S::K * 65536u * 16u);
     if constexpr (S::B == 16 && Op::kLayers > 1)
         if (tid == 32) prefetch_table_share(op.w[1].cb, (uint32_t)S::K * 65536u * 16u);
@@ -664,6 +684,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         mbar_init(acc_full, 1);
         for (int i = 0; i < kInBoxes<Op, BN>; ++i) mbar_init(&in_bar[i], 1);
         *abort_flag = 0;
+        if constexpr (kScaleW) scale_max[0] = scale_max[1] = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -832,6 +853,35 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
         Chunk<S> code_ring[kCodeAhead];
 #pragma unroll
         for (int q = 0; q < kCodeAhead; ++q) code_ring[q] = fetch(dg + NG * q);
+        // kScaleW: the rows' scales, one per lane (rows of the warp's two
+        // row tiles), as far ahead as the codes; divided by 2^E where used
+        float inv = 1.f;
+        uint16_t scale_ring[kCodeAhead];
+        auto fetch_scale = [&](int s) -> uint16_t {
+            const int l = layer_of(s), o = (tile_of(s) - (rt_l & 1)) * 8 + (lane & 15);
+            if (s >= nk || o >= L.out) return (uint16_t)0;  // rows past the layer weigh nothing
+            const uint16_t *sc = op.w[l].scales;
+            return sc ? __ldg(sc + o) : (uint16_t)0x3c00;
+        };
+        if constexpr (kScaleW) {
+            uint32_t c = 0;
+            for (int i = tid - 64; i < op.layers * S::K * 256; i += 128 * NG) finite_absmax_h8(c, scb[i]);
+            c = __reduce_max_sync(0xffffffffu, max(c & 0xffffu, c >> 16));
+            if (lane == 0) atomicMax(scale_max + 1, c);
+            grid_dependency_wait();  // the scales
+#pragma unroll
+            for (int q = 0; q < kCodeAhead; ++q) scale_ring[q] = fetch_scale(dg + NG * q);
+            uint32_t m = 0;
+            for (int l = 0; l < op.layers; ++l)
+                m = max(m, op.w[l].scales ? finite_absmax_share(op.w[l].scales, L.out, tid - 64, 128 * NG) : 0x3c00u);
+            m = __reduce_max_sync(0xffffffffu, m);
+            if (lane == 0) atomicMax(scale_max, m);
+            decoder_barrier(128 * NG);
+            volatile uint32_t *largest = scale_max;
+            const int e = weight_exponent(largest[0], largest[1], S::K);
+            inv = ldexpf(1.f, -e);
+            out.factor = ldexpf(1.f, e);
+        }
         bool ok = true;
         // unrolled by the ring depth so every ring index is static
         for (int k0 = 0; ok && k0 < nown; k0 += kCodeAhead) {
@@ -844,7 +894,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     // the buffer is free once the MMAs of stage s - depth completed
                     if (s >= kWsAStages && !mbar_wait_ns(&empty_a[buf], ((s / kWsAStages) - 1) & 1, kWaitNs)) *abort_v = 1;
                     // a warp leaves together where its lanes act together
-                    if (Pair ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
+                    if ((kScaleW || Pair) ? __any_sync(0xffffffffu, *abort_v != 0) : *abort_v != 0) {
                         ok = false;
                         break;
                     }
@@ -855,7 +905,25 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                     const uint4 *cb = op.w[Op::kLayers > 1 ? layer_of(s) : 0].cb;
                     // kTr: a row past the layer is zero, whatever its padding code selects
                     auto real = [&](int r) { return live && (!kTr || tile_of(s) * 8 + r < L.out); };
-                    if constexpr (kAsyncWeights) {
+                    if constexpr (kScaleW) {
+                        const uint32_t mine = float_to_half_bits(half_bits_to_float(scale_ring[u]) * inv);
+                        auto put = [&](int r, uint4 v) {
+                            const uint32_t h = __shfl_sync(0xffffffffu, mine, (rt_l & 1) * 8 + r);
+                            const __half2 h2 = __half2half2(__ushort_as_half((uint16_t)h));
+                            uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __half2 m = __hmul2(*reinterpret_cast<__half2 *>(&p[j]), h2);
+                                p[j] = real(r) ? *reinterpret_cast<const uint32_t *>(&m) : 0u;
+                            }
+                            *reinterpret_cast<uint4 *>(A + slot_of(r)) = make_uint4(p[0], p[1], p[2], p[3]);
+                        };
+                        uint4 tt[8][S::K];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) gather_terms<S>(code, r, books, cb, tt[r]);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) put(r, sum_round_fast_h8<S::K>(tt[r]));
+                    } else if constexpr (kAsyncWeights) {
                         const uint32_t a0 = smem_u32(A);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
@@ -887,6 +955,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
                 else publish(s);
                 // the next requests follow the fence, which would wait for them
                 code_ring[u] = fetch(s + NG * kCodeAhead);
+                if constexpr (kScaleW) scale_ring[u] = fetch_scale(s + NG * kCodeAhead);
             }
         }
         cp_async_wait<0>();
@@ -906,7 +975,7 @@ gemm_ws_kernel(const __grid_constant__ TensorMaps<Op::kMaps> maps, Geom L, const
             for (int s = max(0, nk - kWsStages); s < nk; ++s)
                 mbar_wait_ns(&full_b[s % kWsStages], (s / kWsStages) & 1, kWaitNs);
     }
-    if constexpr (kTr)
+    if constexpr (kTr && !kScaleW)
         if (op.factor) {
             out.factor = __ldcg(op.factor);
             if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) *op.top = 0u;
@@ -1106,7 +1175,7 @@ constexpr int gemm_ws_smem_bytes()
 {
     constexpr int BB = kWsBookBytes<S, Op>;
     constexpr int NA = kWsAStagesOf<S, BN, BB, Pair>, NB = kWsStagesOf<S, BN, BB, Pair>;
-    return 1024 + NA * kTileABytes + NB * (kBK * BN * 2 / (Pair ? 2 : 1)) + BB + ((Pair ? 3 : 2) * NA + 2 * NB + 1 + kInBoxes<Op, BN>) * 8 + 16;
+    return 1024 + NA * kTileABytes + NB * (kBK * BN * 2 / (Pair ? 2 : 1)) + BB + ((Pair ? 3 : 2) * NA + 2 * NB + 1 + kInBoxes<Op, BN>) * 8 + 32;
 }
 
 // 512-token tiles of two layers' 8x8 codebooks (64 KiB) do not fit.

@@ -30,9 +30,12 @@ cudaError_t copy_rows(const RowCopy *jobs, int n, int T, cudaStream_t s);
 cudaError_t scale_rows(const RowCopy *jobs, int n, int T, float *factor, unsigned *top, bool known, cudaStream_t s);
 
 // The transposed product over one or two layers, gx = sum of W^T g, g0 and g1
-// [out] rows of padded_tokens(T) elements, gx likewise; with `factor`, times
-// *factor, and the workspace's ws_top is cleared.  Its plan works in the first
-// back_plan_bytes of ws.
+// [out] rows of padded_tokens(T) elements, gx likewise.  Layers with one or two
+// 8-bit codebooks have their scales multiplied into the weights; the others'
+// are in g already: with `factor`, the result is multiplied by *factor, and the
+// workspace's ws_top is cleared.  Its plan works in the first back_plan_bytes of
+// ws.
+inline bool back_scales_weights(const aqk::Geom &g) { return g.B == 8 && g.K <= 2; }
 size_t back_plan_bytes(const aqk::Geom &g, int layers, int T);
 cudaError_t launch_back(const aqk::Geom &g, int layers, const aqk::LayerWeights &w0, const uint16_t *g0,
                         const aqk::LayerWeights &w1, const uint16_t *g1, int T, const float *factor, uint16_t *gx,

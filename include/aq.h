@@ -412,11 +412,16 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  * y = diag(s) W x,
  *   gx[i][t] = RN16(sum_o W[o][i] s[o] gy[o][t]),   gy [out][T], gx [in][T],
  * 1 <= T <= 2^22.  The tensor cores take binary16 operands, so s is multiplied
- * into gy: s gy / 2^E is rounded once and 2^E applied to the fp32 sum.  2^E brings
- * the largest finite |s gy| of the call to 2^14 .. 2^15, so that nothing
- * overflows and gradients and scales of any size keep their bits: the rounding
- * is at most 2^-11 of the product plus 2^-39 of the largest one.  (Without scales
- * gy is taken as it is.)  gx overlaps no input.  Together with aq_param_grad
+ * into one of them, divided by 2^E and rounded once; 2^E is applied to the fp32
+ * sum.  E uses binary16's range up, so that nothing overflows and little
+ * becomes subnormal:
+ *  - one or two 8-bit codebooks: into the weights; the largest possible |W s| (of
+ *    the largest scale and codebook entry) and the largest |s| come to at most
+ *    2^15.  The rounding is at most 2^-11 of |W s| plus 2^-25 2^E, for codebook
+ *    entries below 1/2 about 2^-40 of the largest scale;
+ *  - the others: into gy; the largest finite |s gy| of the call comes to 2^14 ..
+ *    2^15.  The rounding is at most 2^-11 of |s gy| plus 2^-39 of the largest.
+ * (Without scales the operand is taken as it is.)  gx overlaps no input.  Together with aq_param_grad
  * this is the backward pass of aq_gemm.  Deterministic; the workspace holds
  * aq_input_grad_workspace_bytes(desc, T) bytes.  Early weight reads: aq_gemv's
  * rule applies, as for aq_gemm_fused.
@@ -470,7 +475,7 @@ aq_status aq_glu_gemm(const aq_layer_desc *desc, const aq_weights *gate, const a
  *   grad_gate = RN16(gy u act'(g)),  grad_up = RN16(gy act(g))     [out][T]
  *   grad_x    = RN16(W_g^T (s_g grad_gate) + W_u^T (s_u grad_up))  [in][T], NULL to skip
  * (of the rounded grad_gate and grad_up; the transposed products as in
- * aq_input_grad, one E for both layers' products).  aq_param_grad(x, grad_gate)
+ * aq_input_grad, with one E for both layers).  aq_param_grad(x, grad_gate)
  * and (x, grad_up) give the scales' and codebooks' gradients.  1 <= T <=
  * 2^22.  Deterministic.  The outputs overlap no input and not
  * one another.  Early weight reads, of both layers: aq_gemv's rule applies, as
