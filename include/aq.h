@@ -418,7 +418,7 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  *  - one or two 8-bit codebooks: into the weights; the largest possible |W s| (of
  *    the largest scale and codebook entry) and the largest |s| come to at most
  *    2^15.  The rounding is at most 2^-11 of |W s| plus 2^-25 2^E, for codebook
- *    entries below 1/2 about 2^-40 of the largest scale;
+ *    entries below 1/2 at most 2^-39 of the largest scale;
  *  - the others: into gy; the largest finite |s gy| of the call comes to 2^14 ..
  *    2^15.  The rounding is at most 2^-11 of |s gy| plus 2^-39 of the largest.
  * (Without scales the operand is taken as it is.)  gx overlaps no input.  Together with aq_param_grad

@@ -430,3 +430,15 @@ def test_the_largest_gradient_is_found_wherever_it_stands(K, B, out, T):
         toks = np.unique([0, 7, 8, 2046, 2047, 2048, 2049, T - 9, T - 2, T - 1, t])
         lr.check(got[:, toks], c.refs[0].back(gy[:, toks]), f"row {r} token {t}")
         assert np.isfinite(got.astype(np.float64)).all()
+
+
+@pytest.mark.parametrize("K,B", SCHEMES)
+@pytest.mark.parametrize("sigma,scale,g", [(3000.0, 1e-3, 0.01), (3000.0, 50.0, 1e-5), (100.0, 2.0 ** -14, 1.0),
+                                           (1e-4, 16000.0, 1.0), (1e-4, 1.0, 1000.0)])
+def test_codebooks_of_any_size(K, B, sigma, scale, g):
+    """Large and small codebook entries, scales and gradients together: nothing
+    overflows, and the error is that of one rounding."""
+    c = Case(520, 264, K, B, 40, layers=2, sigma=sigma, scale=scale)
+    assert all(np.isfinite(r.W).all() for r in c.refs)
+    gy = acts(520, 40, 4, g)
+    _check_rms(c.input_grad(gy), [(c.refs[0], gy)], "input grad")
