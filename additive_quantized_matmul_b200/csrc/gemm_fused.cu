@@ -13,10 +13,10 @@
 //
 // The products are bound by the SM's shared memory and, when calls follow one
 // another, by the power limit (see gemm_ws.cuh).  In series, 2048 tokens:
-// 4096 x 11008 1x16 with residual 183 to 193 us (955 TFLOP/s, 69 % of the tensor
-// rate measured over seconds), gated 2 x 11008 x 4096 2x8 333 to 345 us (1069,
-// 77 %), backward of the gated block, 1x16, 790 to 829 us (891 counting the
-// products computed again, 64 %).  Alone: 160, 298 and 748 us.
+// 4096 x 11008 1x16 with residual 185 to 191 us (976 TFLOP/s, 70 % of the tensor
+// rate measured over seconds), gated 2 x 11008 x 4096 2x8 335 to 345 us (1077,
+// 78 %), backward of the gated block, 1x16, 808 to 850 us (895 counting the
+// products computed again, 65 %).  Alone: 178, 323 and 748 us.
 #include "gemm_ws.cuh"
 #include "layer_ops.cuh"
 
@@ -59,8 +59,9 @@ __device__ __forceinline__ uint4 bytes_from(uint4 a, uint4 b, int m)
 
 // *top = the largest finite |scales[r] src[r][t]| over the jobs, all of as many
 // rows (*top zero before).  A warp takes 4 KiB of a row at a time, its aligned
-// pieces by 16 bytes, the up to seven elements at either end singly.  One pass
-// over the gradients, bound by HBM or, for short ones, the launch.
+// pieces by 16 bytes, the up to seven elements at either end singly.  Bound by the
+// latency of its round trips, two or three a warp: 11008 rows of 2047 tokens (45 MB)
+// 18 us with cold caches, 2.5 TB/s; 4096 rows of 512 tokens 6 us.
 constexpr int kMaxPieces = 256;  // pieces of a row per warp
 
 __global__ void __launch_bounds__(kCopyThreads) scaled_max_kernel(const __grid_constant__ RowCopies jobs, int T)
@@ -166,7 +167,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_rows_kernel(const __grid_co
 // The same for scaled rows of T = pitch, a multiple of 8: every piece is aligned
 // in both arrays.  A warp takes 2 KiB of a row, the next row's share requested
 // before this one's is multiplied; 48 registers leave room for five CTAs an SM
-// (64 and four above).
+// (64 and four above).  Two arrays of 11008 rows and 2048 tokens (90 MB read, 90 MB
+// written, of which 36 MB left L2 meanwhile) 27 us with cold caches.
 __global__ void __launch_bounds__(kCopyThreads, 5) scale_rows_kernel(const __grid_constant__ RowCopies jobs, int T)
 {
     constexpr int kN = kCopyPieces / 32;

@@ -9,7 +9,7 @@
 // wavefronts (8-bit codebooks), then the fixed cost of the split's finish.
 // Inside a graph of cold layers, beside the plain product: 4096 x 4096 1x16 at
 // one token with residual 11.5 us (plain 11.5), 4096 x 11008 2x8 at eight 14.0
-// (13.8); gated 11008 x 4096: 2x8 at one token 13.4 us, at eight 33.3, 1x16 at
+// (13.8); gated 11008 x 4096: 2x8 at one token 13.7 us, at eight 33.6, 1x16 at
 // one 45.2, at sixteen 63.1 (the codeword reads alone take 40).
 #include "gemv_plan.cuh"
 
