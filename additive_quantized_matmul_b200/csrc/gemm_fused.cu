@@ -91,8 +91,14 @@ __global__ void __launch_bounds__(kCopyThreads) scaled_max_kernel(const __grid_c
             m = fmaxf(m, scaled_top(h, c.scales ? half_bits_to_float(__ldg(c.scales + r)) : 1.f));
         }
     }
+    __shared__ uint32_t part[kCopyThreads / 32];
     const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (lane == 0) atomicMax(jobs.top, w);
+    if (lane == 0) part[threadIdx.x >> 5] = w;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const uint32_t all = __reduce_max_sync(0xffffffffu, lane < kCopyThreads / 32 ? part[lane] : 0u);
+        if (lane == 0) atomicMax(jobs.top, all);
+    }
 }
 
 // E of the largest product: 2^14 <= top / 2^E < 2^15, so that none overflows, nor

@@ -416,15 +416,16 @@ aq_status aq_gemm_fused(const aq_layer_desc *desc, const void *packed, const uin
  * sum.  E uses binary16's range up, so that nothing overflows and little
  * becomes subnormal:
  *  - one or two 8-bit codebooks: into the weights; the largest possible |W s| (of
- *    the largest scale and codebook entry) and the largest |s| come to at most
- *    2^15.  The rounding is at most 2^-11 of |W s| plus 2^-25 2^E, for codebook
- *    entries below 1/2 at most 2^-39 of the largest scale;
+ *    the largest scale and codebook entry) and the largest |s| stay below 2^15
+ *    (65504 for entries of 2^13 and more).  The rounding is at most 2^-11 of
+ *    |W s| plus 2^-25 2^E, for codebook entries below 1/2 at most 2^-39 of the
+ *    largest scale;
  *  - the others: into gy; the largest finite |s gy| of the call comes to 2^14 ..
  *    2^15.  The rounding is at most 2^-11 of |s gy| plus 2^-39 of the largest.
- * (Without scales the operand is taken as it is.)  gx overlaps no input.  Together with aq_param_grad
- * this is the backward pass of aq_gemm.  Deterministic; the workspace holds
- * aq_input_grad_workspace_bytes(desc, T) bytes.  Early weight reads: aq_gemv's
- * rule applies, as for aq_gemm_fused.
+ * (Without scales the operand is taken as it is.)  gx overlaps no input.
+ * Together with aq_param_grad this is the backward pass of aq_gemm.
+ * Deterministic; the workspace holds aq_input_grad_workspace_bytes(desc, T)
+ * bytes.  Early weight reads: aq_gemv's rule applies, as for aq_gemm_fused.
  */
 size_t aq_input_grad_workspace_bytes(const aq_layer_desc *desc, int T);
 aq_status aq_input_grad(const aq_layer_desc *desc, const void *packed, const uint16_t *codebooks,
